@@ -43,11 +43,11 @@ def listed():
         # the same product of the audio rows, in the other format, plain
         {"name": "product_mx_audio", "op": "product", "fmt": "mx", "m": 1008, "n": 28672, "k": 5376, "out": "bf16", "swiglu": False},
         # the tiny block with its 32 padding rows
-        {"name": "sandwich_tiny", "op": "sandwich", "rows": 320, "c": 256, "branch": 0, "post": True, "padding": 32},
+        {"name": "sandwich_tiny", "op": "sandwich", "rows": 320, "c": 256, "branch": 0, "post": True, "padding": 32, "mixed": True},
         # after the FFN of the 32k-row sequence, modulated by the next layer's table
-        {"name": "sandwich_32k", "op": "sandwich", "rows": 32768, "c": 5376, "branch": 1, "post": True, "padding": 168},
+        {"name": "sandwich_32k", "op": "sandwich", "rows": 32768, "c": 5376, "branch": 1, "post": True, "padding": 168, "mixed": False},
         # after attention, straight into the FFN's SwiGLU product: h leaves the norm in 4 bits
-        {"name": "chain_nv_ffn_up", "op": "chain", "fmt": "nv", "rows": 4001, "c": 5376, "f": 14336, "padding": 33, "rotate": True},
+        {"name": "chain_nv_ffn_up", "op": "chain", "fmt": "nv", "rows": 4001, "c": 5376, "f": 14336, "padding": 33, "mixed": True, "rotate": True},
     ]
 
 
@@ -66,11 +66,11 @@ def draw(rng):
     if op == "sandwich":
         rows = _log(rng, 1, 32768, 1)
         return {"op": op, "rows": rows, "c": _log(rng, 128, 5376, 128), "branch": rng.randrange(2), "post": rng.random() < 0.7,
-                "padding": rng.randrange(0, rows // 8 + 1)}
+                "padding": rng.randrange(0, rows // 8 + 1), "mixed": rng.random() < 0.5}
     if op == "chain":
         rows = _log(rng, 1, 4096, 1)
         return {"op": op, "fmt": fmt, "rows": rows, "c": _log(rng, 128, 5376, 128), "f": _log(rng, 128, 14336, 128),
-                "padding": rng.randrange(0, rows // 8 + 1), "rotate": rng.random() < 0.5}
+                "padding": rng.randrange(0, rows // 8 + 1), "mixed": rng.random() < 0.5, "rotate": rng.random() < 0.5}
     m, rotate = _log(rng, 1, 8192, 1), rng.random() < 0.4
     out = rng.choice(["bf16", "bf16", "fp32"])
     if op == "linear":
@@ -102,13 +102,19 @@ def _weight(g, n, k):
 
 
 def _modulated(g, c, padding):
-    """Packed rows' residual stream, the block's output, tags (tag -1: padding), timestep indices and a table."""
+    """Packed rows' residual stream, the block's output, tags (tag -1: padding), timestep indices and a table.
+    The sequence is packed as the model packs it: text, then audio, then video rows, padding last; "mixed" draws
+    each row's timestep index by itself, as two-time conditioning does."""
     n, ch = c["rows"], c["c"]
-    tag = torch.randint(0, 4, (n,), generator=g, device=DEV, dtype=torch.int32)
+    tag = torch.full((n,), 3, device=DEV, dtype=torch.int32)
+    tag[:n // 10] = 2
+    tag[:n // 16] = 0
+    tidx = (tag == 2).to(torch.int32)
+    if c["mixed"]:
+        tidx = torch.randint(0, 2, (n,), generator=g, device=DEV, dtype=torch.int32)
     if padding:
         tag[n - padding:] = -1
-    return {"x": (1.5 * _rand(g, n, ch)).to(torch.bfloat16), "y": _rows(g, n, ch), "tag": tag,
-            "tidx": torch.randint(0, 2, (n,), generator=g, device=DEV, dtype=torch.int32),
+    return {"x": (1.5 * _rand(g, n, ch)).to(torch.bfloat16), "y": _rows(g, n, ch), "tag": tag, "tidx": tidx,
             "table": 0.3 * _rand(g, 4, 2, 6, ch), "next": 0.3 * _rand(g, 4, 2, 6, ch),
             "gain": (1 + 0.1 * _rand(g, ch)).to(torch.bfloat16), "alpha": 0.7}
 
