@@ -250,6 +250,109 @@ H3BLK_API int h3blk_gemm_s8_s32(int64_t M, int N, int K, const int8_t* A, const 
  * (K a multiple of 64, N a multiple of 128). */
 H3BLK_API int h3blk_gemm_bf16(int64_t M, int N, int K, const void* A, const void* B, void* C, void* stream);
 
+/* --------------------------------------------- 4-bit floats (microscaled) */
+/* A matrix [rows, K] in microscaled 4-bit floats: the step below the W8A8
+ * linears ("HyperFlow H3 Flash ...", "How it got smaller and faster"; the pages
+ * stop at int8, so the formats here are this library's reading). A value is
+ *     e2m1 code * block scale * row_scale[row],
+ * e2m1 codes standing for 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.
+ *   format     H3BLK_FP4_MX: blocks of 32 channels, power-of-two scales (e8m0)
+ *              H3BLK_FP4_NV: blocks of 16 channels, e4m3 scales
+ *   rows, K    rows >= 0; K a multiple of 32
+ *   codes      [rows][K / 2] bytes, channel 2 i in the low nibble of byte i
+ *   scales     atoms of 128 rows x 4 blocks (512 bytes): the scale of row r,
+ *              block b is byte (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4 of atom
+ *              (r / 128) * ceil(blocks / 4) + b / 4, blocks = ceil(K / 32 or 16).
+ *              Bytes of blocks past K in a row's last atom are finite scales
+ *              (never NaN); bytes of rows past the last are not written or used.
+ *   row_scale  fp32 [rows]
+ * Device pointers, caller-owned, 16-byte aligned. */
+#define H3BLK_FP4_MX 0
+#define H3BLK_FP4_NV 1
+typedef struct {
+  int format;
+  int K;
+  int64_t rows;
+  void* codes;
+  void* scales;
+  float* row_scale;
+} h3blk_fp4;
+
+/* Bytes of the three buffers of a [rows, K] matrix. INVALID_ARG for an unknown
+ * format, rows < 0, K < 1 or K not a multiple of 32. */
+H3BLK_API int h3blk_fp4_bytes(int format, int64_t rows, int K, size_t* codes, size_t* scales, size_t* row_scale);
+
+/* Quantises bf16 rows [out->rows, out->K] (row stride ld_in elements, >= K and
+ * a multiple of 8) into `out`. Codes are rounded to nearest, ties to the even
+ * code, and saturate at 6.
+ *   MX: block scale 2^e, e the smallest with amax <= 7 * 2^e (and e >= -126);
+ *       row_scale = 1.
+ *   NV: row_scale = 2^E, E the smallest with the row's amax <= 2688 * 2^E (0
+ *       for a zero row, and E >= -126); block scale = amax / 2^E / 6 in e4m3.
+ * Every factor before the codes' rounding is a power of two or divided
+ * exactly, so codes and scales of given values are the same bits on any
+ * implementation. rotate != 0 (K a multiple of 128) first applies the block-128
+ * Hadamard transform of h3blk_rotate_quantize, its 1/sqrt(128) in row_scale.
+ * A block that holds an infinity or a NaN (for rotate: whose 128 channels do)
+ * gets the NaN scale; the other blocks are quantised as if it were zero.
+ * UNSUPPORTED when K > 16384. */
+H3BLK_API int h3blk_quantize_fp4(const void* in_bf16, int64_t ld_in, int rotate, const h3blk_fp4* out, void* stream);
+
+/* The values `in` stands for (a rotated matrix stays rotated), rounded once to
+ * the output type: H3BLK_BF16 or H3BLK_F32 [rows, K] with row stride ld_out
+ * (>= K, a multiple of 8). */
+#define H3BLK_BF16 0
+#define H3BLK_F32 1
+H3BLK_API int h3blk_dequantize_fp4(const h3blk_fp4* in, int out_type, void* out, int64_t ld_out, void* stream);
+
+/* Product of two 4-bit matrices of the same format and K on the tensor cores,
+ * fp32 accumulation, output bf16 or fp32 with row stride ld_out (a multiple of 8):
+ *   H3BLK_FP4_STORE   out[m, n] = A[m] . B[n]           [A->rows, B->rows]
+ *   H3BLK_FP4_SWIGLU  out[m, n] = silu(A[m] . B[n]) * (A[m] . B[F + n])
+ *                     [A->rows, F], F = B->rows / 2 (the layout of w13)
+ * A->rows may be 0. UNSUPPORTED unless the output's columns are a multiple of
+ * 8 (STORE) or 128 (SWIGLU). `out` must not overlap the operands. */
+#define H3BLK_FP4_STORE 0
+#define H3BLK_FP4_SWIGLU 1
+H3BLK_API int h3blk_gemm_fp4(const h3blk_fp4* A, const h3blk_fp4* B, int epilogue, int out_type, void* out,
+                             int64_t ld_out, void* stream);
+
+/* ------------------------------------------------------- sandwich norm */
+/* The norms after and before a block, fused with its gate and residual: y is
+ * the output of an attention (branch 0) or feed-forward (branch 1) step whose
+ * linears ran outside h3blk_forward, x the residual stream.
+ *   p     = post_norm ? rmsnorm(y, post_eps) * post_gain : y
+ *   x_out = x + branch_scale * gate * p
+ *   h     = rmsnorm(x_out, norm_eps) * (1 + scale) + shift   (before x_out is rounded)
+ * gate is gate1 (branch 0) or gate2 (branch 1) of the row's (tag, tidx) in
+ * mod_table; shift / scale are shift2 / scale2 of norm_table after attention,
+ * shift1 / scale1 of norm_table (the next layer's table) after the
+ * feed-forward step. Rows with tag -1, and rows whose indices lie outside the
+ * table, get zero gate, shift and scale (x_out = x).
+ *   x, y, x_out  bf16 [n_rows, hidden], hidden a multiple of 128 (UNSUPPORTED
+ *                otherwise, and above 16384); x_out may be x itself, and
+ *                overlaps nothing else
+ *   post_gain    bf16 [hidden], may be NULL (ones); only with post_norm
+ *   norm_table   fp32 [n_tags][n_t][6][hidden]; NULL: no h is made
+ *   h            bf16 [n_rows, hidden], or
+ *   h_fp4        h as the operand of h3blk_gemm_fp4, quantised from its fp32
+ *                values as by h3blk_quantize_fp4 (rotate as there). Exactly one
+ *                of the two with norm_table, none without. */
+typedef struct {
+  int64_t n_rows;
+  int hidden, n_tags, n_t;
+  int branch;
+  int post_norm;
+  float post_eps, norm_eps, branch_scale;
+  const void *x, *y, *post_gain;
+  const int32_t *tag, *tidx;
+  const float *mod_table, *norm_table;
+  void *x_out, *h;
+  const h3blk_fp4* h_fp4;
+  int rotate;
+} h3blk_sandwich;
+H3BLK_API int h3blk_sandwich_norm(const h3blk_sandwich* args, void* stream);
+
 /* ------------------------------------------------- modulation-table producer */
 /* The step before the block: turns the distinct timesteps of a forward into the
  * AdaLN table h3blk_forward reads.

@@ -33,7 +33,12 @@ EXPORTS = ["h3blk_create", "h3blk_destroy", "h3blk_workspace_bytes", "h3blk_stag
            "h3blk_model_graph_create", "h3blk_graph_launch", "h3blk_graph_info", "h3blk_graph_destroy",
            "h3blk_ulysses_buffer_bytes", "h3blk_ulysses_workspace_bytes", "h3blk_ulysses_qkv",
            "h3blk_ulysses_attention", "h3blk_ulysses_out", "h3blk_set_attention_density",
-           "h3blk_selftest_wait", "h3blk_set_debug_accumulators"]
+           "h3blk_selftest_wait", "h3blk_set_debug_accumulators", "h3blk_fp4_bytes", "h3blk_quantize_fp4",
+           "h3blk_dequantize_fp4", "h3blk_gemm_fp4", "h3blk_sandwich_norm"]
+
+H3BLK_FP4_MX, H3BLK_FP4_NV = 0, 1
+H3BLK_BF16, H3BLK_F32 = 0, 1
+H3BLK_FP4_STORE, H3BLK_FP4_SWIGLU = 0, 1
 
 H3BLK_MAX_RANKS = 8
 
@@ -94,6 +99,19 @@ class h3blk_ulysses(C.Structure):
     _fields_ = [("world", C.c_int), ("rank", C.c_int), ("qkv", C.c_void_p * 8), ("o", C.c_void_p * 8)]
 
 
+class h3blk_fp4(C.Structure):
+    _fields_ = [("format", C.c_int), ("K", C.c_int), ("rows", C.c_int64), ("codes", C.c_void_p),
+                ("scales", C.c_void_p), ("row_scale", C.c_void_p)]
+
+
+class h3blk_sandwich(C.Structure):
+    _fields_ = [("n_rows", C.c_int64), ("hidden", C.c_int), ("n_tags", C.c_int), ("n_t", C.c_int),
+                ("branch", C.c_int), ("post_norm", C.c_int), ("post_eps", C.c_float), ("norm_eps", C.c_float),
+                ("branch_scale", C.c_float), ("x", C.c_void_p), ("y", C.c_void_p), ("post_gain", C.c_void_p),
+                ("tag", C.c_void_p), ("tidx", C.c_void_p), ("mod_table", C.c_void_p), ("norm_table", C.c_void_p),
+                ("x_out", C.c_void_p), ("h", C.c_void_p), ("h_fp4", C.POINTER(h3blk_fp4)), ("rotate", C.c_int)]
+
+
 class H3BlkError(RuntimeError):
     def __init__(self, fn, status):
         super().__init__(f"{fn} failed: status {status} ({error_string(status)})")
@@ -117,6 +135,11 @@ def _load():
         "h3blk_rotate_quantize": (i32, [i64, i32, vp, vp, vp, vp]),
         "h3blk_gemm_s8_s32": (i32, [i64, i32, i32, vp, vp, vp, vp]),
         "h3blk_gemm_bf16": (i32, [i64, i32, i32, vp, vp, vp, vp]),
+        "h3blk_fp4_bytes": (i32, [i32, i64, i32, C.POINTER(sz), C.POINTER(sz), C.POINTER(sz)]),
+        "h3blk_quantize_fp4": (i32, [vp, i64, i32, C.POINTER(h3blk_fp4), vp]),
+        "h3blk_dequantize_fp4": (i32, [C.POINTER(h3blk_fp4), i32, vp, i64, vp]),
+        "h3blk_gemm_fp4": (i32, [C.POINTER(h3blk_fp4), C.POINTER(h3blk_fp4), i32, i32, vp, i64, vp]),
+        "h3blk_sandwich_norm": (i32, [C.POINTER(h3blk_sandwich), vp]),
         "h3blk_error_string": (C.c_char_p, [i32]),
         "h3blk_version": (i32, []),
         "h3blk_set_kernel_events": (i32, [vp, C.POINTER(vp), i32]),
@@ -243,6 +266,29 @@ def h3blk_gemm_s8_s32(M, N, K, A, B, Cp, stream) -> int:
 
 def h3blk_gemm_bf16(M, N, K, A, B, Cp, stream) -> int:
     return _lib.h3blk_gemm_bf16(M, N, K, A, B, Cp, stream)
+
+
+def h3blk_fp4_bytes(fmt, rows, K) -> tuple[int, int, int]:
+    a, b, c = C.c_size_t(), C.c_size_t(), C.c_size_t()
+    _check("h3blk_fp4_bytes", _lib.h3blk_fp4_bytes(fmt, rows, K, C.byref(a), C.byref(b), C.byref(c)))
+    return a.value, b.value, c.value
+
+
+def h3blk_quantize_fp4(in_bf16, ld_in, rotate, out: h3blk_fp4, stream) -> int:
+    """Raw call (pointers are ints); returns the status code."""
+    return _lib.h3blk_quantize_fp4(in_bf16, ld_in, rotate, out, stream)
+
+
+def h3blk_dequantize_fp4(q: h3blk_fp4, out_type, out, ld_out, stream) -> int:
+    return _lib.h3blk_dequantize_fp4(q, out_type, out, ld_out, stream)
+
+
+def h3blk_gemm_fp4(a: h3blk_fp4, b: h3blk_fp4, epilogue, out_type, out, ld_out, stream) -> int:
+    return _lib.h3blk_gemm_fp4(a, b, epilogue, out_type, out, ld_out, stream)
+
+
+def h3blk_sandwich_norm(args: h3blk_sandwich, stream) -> int:
+    return _lib.h3blk_sandwich_norm(args, stream)
 
 
 def h3blk_set_kernel_events(handle, events) -> None:

@@ -131,6 +131,63 @@ cudaError_t launch_rope_table(const int32_t* pos, int64_t n, const RopeTable& ro
                               cudaStream_t s);
 inline size_t rope_table_bytes(int64_t n, int pairs) { return (size_t)n * pairs * sizeof(float2); }
 
+// ---------------------------------------------------------------- 4-bit linears
+// Rows of bf16 [rows, K] (row stride ld) -> microscaled 4-bit floats (fp4.cuh);
+// nv: blocks of 16 with e4m3 scales, otherwise blocks of 32 with e8m0 scales.
+struct Fp4QuantArgs {
+  const __nv_bfloat16* in;
+  int64_t ld, rows;
+  int K;
+  bool nv, rotate;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* row_scale;
+};
+cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, cudaStream_t s);
+struct Fp4DequantArgs {
+  const uint8_t* codes;
+  uint8_t* scales;
+  const float* row_scale;
+  int64_t rows;
+  int K;
+  bool nv, f32;
+  void* out;
+  int64_t ld;
+};
+cudaError_t launch_dequantize_fp4(const Fp4DequantArgs& a, cudaStream_t s);
+
+// out[m, n] = A[m] . B[n] over 4-bit operands of one format; swiglu: B holds
+// 2 N rows (gate, then up) and out = silu(gate) * up.
+struct Fp4GemmArgs {
+  const uint8_t *a_codes, *b_codes;
+  const uint8_t *a_scales, *b_scales;
+  const float *a_row, *b_row;
+  int64_t M;
+  int N;   // output columns
+  int K;
+  bool nv, swiglu, f32;
+  void* out;
+  int64_t ld;
+};
+cudaError_t launch_gemm_fp4(const Fp4GemmArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms,
+                            cudaStream_t s);
+
+// ---------------------------------------------------------------- sandwich norm
+struct SandwichArgs {
+  const __nv_bfloat16 *x, *y, *post_gain;
+  const int32_t *tag, *tidx;
+  const float *table, *norm_table;  // norm_table null: no h
+  int64_t rows;
+  int C, n_tags, n_t, gate_idx, shift_idx;  // the scale vector follows the shift
+  bool post_norm;
+  float post_eps, norm_eps, branch_scale;
+  __nv_bfloat16 *x_out, *h;  // h null: 4-bit h below
+  bool nv, rotate;
+  uint8_t *codes, *scales;
+  float* row_scale;
+};
+cudaError_t launch_sandwich(const SandwichArgs& a, cudaStream_t s);
+
 // ---------------------------------------------------------------- attention
 struct AttnArgs {
   const __nv_bfloat16* qkv;  // [N, 3*H*D]: q heads, k heads, v heads

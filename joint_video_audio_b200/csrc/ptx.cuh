@@ -126,6 +126,14 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
+// 3-D tiled load of a box (see tma_load_2d).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- CTA pairs (cluster of 2)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -155,6 +163,16 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
       "[%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y)
+      : "memory");
+}
+
+// 3-D form of tma_load_2d_pair.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar_cluster, int x, int y,
+                                                 int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 
@@ -313,6 +331,63 @@ __device__ __forceinline__ void mma_commit_pair_w(uint64_t* bar, uint16_t cta_ma
       ::"r"(smem_u32(bar)), "h"(cta_mask)
       : "memory");
 }
+// Block-scaled 4-bit products, D[tmem] (+)= (A SA)(B SB)^T with e2m1 A / B in
+// shared memory (K = 64 per product, two values a byte), fp32 accumulators and
+// the block scales in tensor memory: NV = e4m3 scales of 16 values (four per
+// row), otherwise e8m0 scales of 32 values (two per row, which two of the
+// column's four bytes being the instruction descriptor's scale ids).
+template <bool NV>
+__device__ __forceinline__ void mma_fp4_ss_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+  if (NV)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t" H3_ELECT_PRED
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t" H3_ELECT_PRED
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+template <bool NV>
+__device__ __forceinline__ void mma_fp4_ss_pair_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                  uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+  if (NV)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t" H3_ELECT_PRED
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t" H3_ELECT_PRED
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+// Copies 512 bytes (32 rows of 16) from shared memory into four 32-bit columns
+// of tensor memory, row i to lanes i, i + 32, i + 64 and i + 96: one atom of
+// block scales where the products read it. The pair form copies each CTA's own
+// atom into its own tensor memory. A later product of the same thread sees it.
+__device__ __forceinline__ void tmem_cp_scales_w(uint32_t taddr, uint64_t desc) {
+  asm volatile("{\n\t.reg .pred e;\n\t" H3_ELECT_PRED "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(
+                   taddr),
+               "l"(desc)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_cp_scales_pair_w(uint32_t taddr, uint64_t desc) {
+  asm volatile("{\n\t.reg .pred e;\n\t" H3_ELECT_PRED "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(
+                   taddr),
+               "l"(desc)
+               : "memory");
+}
 // A barrier wait whose result is the same in every lane of the warp: it fails
 // for the warp if it failed in any lane.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -432,6 +507,24 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr, uint32_t lbo_
   return d;
 }
 
+// Descriptor of one unswizzled 512-byte scale atom: 32 rows of 16 bytes, the
+// 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_atom_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
+  d |= (uint64_t)(128u >> 4) << 32;  // stride between 8-row groups
+  d |= (uint64_t)1 << 46;            // descriptor version (sm_100)
+  return d;
+}
+
+// Instruction descriptor of a block-scaled 4-bit tcgen05.mma: e2m1 A and B
+// (format 1), both K-major; ue8m0 picks power-of-two scales over e4m3 ones;
+// sf_id is the first byte of the scale columns that this product reads.
+__host__ __device__ constexpr uint32_t make_idesc_fp4(int m, int n, bool ue8m0, uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((ue8m0 ? 1u : 0u) << 23) |
+         ((uint32_t)(m >> 4) << 24) | (sf_id << 29);
+}
+
 // Instruction descriptor of a dense tcgen05.mma with M = 128.
 //   kind::f16 with bf16 A/B and fp32 D:  c_fmt = 1, ab_fmt = 1
 //   kind::i8  with s8 A/B and s32 D:     c_fmt = 2, ab_fmt = 1
@@ -459,6 +552,11 @@ __device__ __forceinline__ void f2_unpack(uint64_t r, float& a, float& b) {
 __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {

@@ -1,0 +1,184 @@
+"""torch-tensor marshalling of the 4-bit linear path and the sandwich norm
+(no arithmetic here): include/h3blk.h states the formats and the formulas."""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import _binding as B
+
+FORMATS = {"mx": B.H3BLK_FP4_MX, "nv": B.H3BLK_FP4_NV}
+_OUT = {torch.bfloat16: B.H3BLK_BF16, torch.float32: B.H3BLK_F32}
+
+
+def _call(fn, name, dev, *args):
+    """fn(*args, stream) on `dev`'s current stream, with `dev` current."""
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != B.H3BLK_OK:
+        raise B.H3BlkError(name, st)
+
+
+def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16, cols=None) -> int:
+    """Row stride of a 2-D CUDA tensor with unit column stride; ValueError otherwise."""
+    if not t.is_cuda or t.dim() != 2 or t.dtype != dtype:
+        raise ValueError(f"{name}: expected a 2-D {dtype} CUDA tensor, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    rows, k = t.shape
+    if cols is not None and k != cols:
+        raise ValueError(f"{name}: expected {cols} columns, got {k}")
+    if k > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: its rows are not contiguous")
+    if rows < 2:
+        return -(-k // 8) * 8
+    if t.stride(0) < k or t.stride(0) % 8:
+        raise ValueError(f"{name}: row stride {t.stride(0)} is not a multiple of 8 of at least {k}")
+    return t.stride(0)
+
+
+class Fp4Tensor:
+    """A [rows, K] matrix in microscaled 4-bit floats on the GPU (h3blk_fp4).
+
+    codes      uint8 [rows, K / 2], two e2m1 codes a byte
+    scales     uint8 [..., 512] atoms of 128 rows x 4 block scales
+    row_scale  fp32 [rows]
+    """
+
+    def __init__(self, rows: int, K: int, fmt: str = "nv", device="cuda"):
+        if fmt not in FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(FORMATS)}, got {fmt!r}")
+        nc, ns, nr = B.h3blk_fp4_bytes(FORMATS[fmt], rows, K)
+        self.fmt, self.shape = fmt, (rows, K)
+        # one buffer; every part starts on a 256-byte boundary
+        self._at = (0, -(-nc // 256) * 256, -(-nc // 256) * 256 + -(-ns // 256) * 256)
+        self._len = (nc, ns, nr)
+        self.buffer = torch.empty(max(256, self._at[2] + nr), dtype=torch.uint8, device=device)
+        p = self.buffer.data_ptr()
+        self.c = B.h3blk_fp4(format=FORMATS[fmt], K=K, rows=rows, codes=p + self._at[0], scales=p + self._at[1],
+                             row_scale=p + self._at[2])
+
+    def _part(self, i):
+        return self.buffer[self._at[i]:self._at[i] + self._len[i]]
+
+    @property
+    def device(self):
+        return self.buffer.device
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self._part(0).view(self.shape[0], self.shape[1] // 2)
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._part(1).view(-1, 512)
+
+    @property
+    def row_scale(self) -> torch.Tensor:
+        return self._part(2).view(torch.float32)
+
+    def __repr__(self):
+        return f"Fp4Tensor({self.shape[0]}, {self.shape[1]}, {self.fmt!r}, {self.device})"
+
+
+def quantize_fp4(x: torch.Tensor, fmt: str = "nv", rotate: bool = False, out: Fp4Tensor | None = None) -> Fp4Tensor:
+    """bf16 [rows, K] (rows may be strided) -> microscaled 4-bit floats.
+
+    fmt "mx": blocks of 32 with power-of-two scales; "nv": blocks of 16 with
+    e4m3 scales and a power-of-two scale per row. rotate: the block-128 Hadamard
+    transform of the W8A8 path first (rotate both operands of a product, or
+    neither). h3blk_quantize_fp4."""
+    ld = _rows(x, "x")
+    if out is None:
+        out = Fp4Tensor(x.shape[0], x.shape[1], fmt, x.device)
+    elif out.fmt != fmt or out.shape != tuple(x.shape) or out.device != x.device:
+        raise ValueError(f"out: expected {fmt} {tuple(x.shape)} on {x.device}, got {out}")
+    if x.shape[0]:
+        _call(B.h3blk_quantize_fp4, "h3blk_quantize_fp4", x.device, x.data_ptr(), ld, int(rotate), out.c)
+    return out
+
+
+def dequantize_fp4(q: Fp4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values `q` stands for, bf16 or fp32 [rows, K] (h3blk_dequantize_fp4)."""
+    if dtype not in _OUT:
+        raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    out = _output(out, q.shape[0], q.shape[1], dtype, q.device)
+    ld = _rows(out, "out", dtype)
+    if q.shape[0]:
+        _call(B.h3blk_dequantize_fp4, "h3blk_dequantize_fp4", q.device, q.c, _OUT[dtype], out.data_ptr(), ld)
+    return out
+
+
+def _output(out, rows, cols, dtype, device):
+    if out is None:
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+    if tuple(out.shape) != (rows, cols) or out.dtype != dtype or out.device != device:
+        raise ValueError(f"out: expected {dtype} {(rows, cols)} on {device}, got {out.dtype} {tuple(out.shape)} on {out.device}")
+    return out
+
+
+def gemm_fp4(a: Fp4Tensor, b: Fp4Tensor, swiglu: bool = False, dtype=torch.bfloat16,
+             out: torch.Tensor | None = None) -> torch.Tensor:
+    """A [M, K] B [N, K]^T of two 4-bit matrices -> bf16 or fp32 [M, N]; with
+    swiglu, B holds the gate rows, then the up rows, and the result is
+    silu(gate) * up [M, N / 2] (h3blk_gemm_fp4)."""
+    if a.fmt != b.fmt or a.shape[1] != b.shape[1] or a.device != b.device:
+        raise ValueError(f"operands do not match: {a} and {b}")
+    if dtype not in _OUT:
+        raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    out = _output(out, a.shape[0], b.shape[0] // 2 if swiglu else b.shape[0], dtype, a.device)
+    ld = _rows(out, "out", dtype)
+    if a.shape[0]:
+        _call(B.h3blk_gemm_fp4, "h3blk_gemm_fp4", a.device, a.c, b.c,
+              B.H3BLK_FP4_SWIGLU if swiglu else B.H3BLK_FP4_STORE, _OUT[dtype], out.data_ptr(), ld)
+    return out
+
+
+def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post_norm: bool = True, post_gain=None,
+                  post_eps: float = 1e-5, norm_eps: float = 1e-5, branch_scale: float = 1.0, h: str | None = "bf16",
+                  rotate: bool = False, x_out=None):
+    """The norms after and before a block fused with its gate and residual:
+
+      x_out = x + branch_scale * gate * (rmsnorm(y) * post_gain)    (y itself without post_norm)
+      h     = rmsnorm(x_out) * (1 + scale) + shift
+
+    branch 0 follows attention (gate1, then shift2 / scale2 of `table`); branch
+    1 follows the feed-forward step (gate2, then shift1 / scale1 of
+    `next_table`, the next layer's). h: "bf16", "mx" / "nv" (an Fp4Tensor, as
+    quantize_fp4 of h's fp32 values; rotate as there) or None; without a next
+    table there is no h after branch 1. x_out may be x. Returns (x_out, h).
+    h3blk_sandwich_norm."""
+    if x.dim() != 2 or table.dim() != 4:
+        raise ValueError("expected x [rows, hidden] and table [n_tags, n_t, 6, hidden]")
+    n, c = x.shape
+    dev = x.device
+    if x_out is None:
+        x_out = torch.empty_like(x)
+    norm_table = (next_table if branch else table) if h is not None else None
+    for name, t, dt, shape in (("x", x, torch.bfloat16, (n, c)), ("y", y, torch.bfloat16, (n, c)),
+                               ("x_out", x_out, torch.bfloat16, (n, c)), ("tag", tag, torch.int32, (n,)),
+                               ("tidx", tidx, torch.int32, (n,)),
+                               ("table", table, torch.float32, (*table.shape[:2], 6, c)),
+                               ("next_table", norm_table, torch.float32, tuple(table.shape)),
+                               ("post_gain", post_gain, torch.bfloat16, (c,))):
+        if t is not None and (not t.is_cuda or t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous()
+                              or t.device != dev):
+            raise ValueError(f"{name}: expected {dt} {shape} contiguous on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    out = None
+    if norm_table is not None:
+        out = torch.empty_like(x) if h == "bf16" else Fp4Tensor(n, c, h, dev)
+    fp4 = out if isinstance(out, Fp4Tensor) else None
+    if rotate and fp4 is None:
+        raise ValueError("rotate is for an h in 4 bits")
+    a = B.h3blk_sandwich(n_rows=n, hidden=c, n_tags=table.shape[0], n_t=table.shape[1], branch=branch,
+                         post_norm=int(post_norm), post_eps=post_eps, norm_eps=norm_eps, branch_scale=branch_scale,
+                         x=x.data_ptr(), y=y.data_ptr(), post_gain=None if post_gain is None else post_gain.data_ptr(),
+                         tag=tag.data_ptr(), tidx=tidx.data_ptr(), mod_table=table.data_ptr(),
+                         norm_table=None if norm_table is None else norm_table.data_ptr(), x_out=x_out.data_ptr(),
+                         h=out.data_ptr() if out is not None and fp4 is None else None,
+                         h_fp4=None if fp4 is None else C.pointer(fp4.c), rotate=int(rotate))
+    if n:
+        _call(B.h3blk_sandwich_norm, "h3blk_sandwich_norm", dev, a)
+    return x_out, out
