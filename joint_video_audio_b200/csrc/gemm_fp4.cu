@@ -212,6 +212,314 @@ __global__ void __launch_bounds__(kFewThreads)
   if (warp == 1) tmem_dealloc(tmem, Cfg::kTmemCols);
 }
 
+// ------------------------------------------------------------------ CTA pairs
+// Products of many rows: persistent clusters of two CTAs, 256 x 256 cluster
+// tiles, products of M = 256, N = 256, K = 64 over both SMs' shared memory
+// (each SM stages its 128 rows of A and half of the tile's weight rows, the
+// scales of its A rows and those of all 256 weight rows). SwiGLU tiles hold
+// 128 gate rows and the 128 up rows that go with them.
+//
+// Tensor memory has 512 columns. Two 256-column accumulators would leave none
+// for the scales, so the second one starts at column 208, over the last 48 of
+// the first, and the scales take the 48 columns behind it. An epilogue warp
+// reads its share of the overlapped columns first and then lets the next
+// tile's products begin; the rest of its tile overlaps them.
+//
+// The scale columns are two slots of 24: 128 channels of NV scales (two
+// products), or 256 of MX scales (four). A slot is rewritten once the products
+// that read it have completed.
+constexpr int kPairThreads = 320;  // producer, issuer, eight epilogue warps
+constexpr int kPairEpiWarps = 8;
+constexpr int kAcc1 = 208, kScaleCol = 464, kSlotCols = 24;
+constexpr int kGroupN = 12;  // tile raster: 12 N-tiles share each pass over M
+
+template <int FMT>
+struct PairCfg {
+  static constexpr int kAtoms = atoms_per_stage(FMT);
+  static constexpr int kScaleBytes = kAtoms * 512;  // of 128 rows
+  static constexpr int kStageBytes = 2 * kTile + 3 * kScaleBytes;
+  static constexpr int kStages = FMT == kFp4NV ? 5 : 6;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 256;
+};
+
+struct Tile {
+  int m, n;
+};
+__device__ __forceinline__ Tile pair_tile(int t, int tiles_m, int tiles_n) {
+  const int group = t / (kGroupN * tiles_m);
+  const int first = group * kGroupN;
+  const int gn = min(kGroupN, tiles_n - first);
+  const int i = t - group * kGroupN * tiles_m;
+  return {i / gn, first + i % gn};
+}
+
+// One row's 32 columns from `col`, as far as N reaches (a multiple of 8).
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* dst, const float (&v)[32], int col, int N) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (col + 8 * i >= N) break;
+    if (sizeof(T) == 2) {
+      reinterpret_cast<uint4*>(dst)[i] =
+          make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                     pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    } else {
+      reinterpret_cast<float4*>(dst)[2 * i] = make_float4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
+      reinterpret_cast<float4*>(dst)[2 * i + 1] = make_float4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
+    }
+  }
+}
+// Accumulators times the row scales of A's row and of 32 weight rows from `rb`
+// (of which those past `left` are absent).
+__device__ __forceinline__ void scale_chunk(const uint32_t (&r)[32], float ra, const float* rb, int left, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 b = 4 * i < left ? __ldg(reinterpret_cast<const float4*>(rb) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[4 * i] = __uint_as_float(r[4 * i]) * ra * b.x;
+    v[4 * i + 1] = __uint_as_float(r[4 * i + 1]) * ra * b.y;
+    v[4 * i + 2] = __uint_as_float(r[4 * i + 2]) * ra * b.z;
+    v[4 * i + 3] = __uint_as_float(r[4 * i + 3]) * ra * b.w;
+  }
+}
+
+template <int FMT, bool SWIGLU, typename T>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmAS, const __grid_constant__ CUtensorMap tmBS,
+                         const Fp4GemmArgs p) {
+  using Cfg = PairCfg<FMT>;
+  constexpr int kStages = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  // stage: A tile, B tile, A scales, scales of the tile's first and second 128 weight rows
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)kStages * Cfg::kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* sfree = empty + kStages;
+  uint64_t* tfull = sfree + 2;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_word = reinterpret_cast<int*>(drain + 2);
+  volatile int* abort = abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+  const int tiles_m = (int)((p.M + 255) / 256);
+  const int tiles_n = SWIGLU ? p.N / 128 : (p.N + 255) / 256;
+  const int num_tiles = tiles_m * tiles_n;
+  const int num_kb = (p.K + kBlockK - 1) / kBlockK;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);   // the first CTA's producer arrives; both CTAs' bytes complete it
+      mbar_init(&empty[i], 1);  // one commit of the issuer
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfree[i], 1);
+      mbar_init(&tfull[i], 1);
+    }
+    mbar_init(tempty, 2 * kPairEpiWarps);
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmAS);
+    tma_prefetch_desc(&tmBS);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers are initialised and their tensor memory allocated
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer (both CTAs)
+    if (lane == 0) {
+      const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+      int stage = 0;
+      uint32_t phase = 0;
+      long issued = 0;
+      bool ok = true;
+      for (int t = cluster; t < num_tiles && ok; t += n_clusters) {
+        const Tile tc = pair_tile(t, tiles_m, tiles_n);
+        const int ya = tc.m * 256 + (int)rank * 128;
+        const int b0 = SWIGLU ? tc.n * 128 : tc.n * 256, b1 = SWIGLU ? p.N + b0 : b0 + 128;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort)) {
+            *abort = 1;
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + (size_t)stage * Cfg::kStageBytes;
+          const uint32_t bar = full0 + 8u * stage;
+          if (rank == 0) mbar_expect_tx(&full[stage], 2 * Cfg::kStageBytes);
+          tma_load_2d_pair(st, &tmA, bar, kb * kRowBytes, ya);
+          tma_load_2d_pair(st + kTile, &tmB, bar, kb * kRowBytes, rank ? b1 : b0);
+          tma_load_3d_pair(st + 2 * kTile, &tmAS, bar, 0, kb * Cfg::kAtoms, ya >> 7);
+          tma_load_3d_pair(st + 2 * kTile + Cfg::kScaleBytes, &tmBS, bar, 0, kb * Cfg::kAtoms, b0 >> 7);
+          tma_load_3d_pair(st + 2 * kTile + 2 * Cfg::kScaleBytes, &tmBS, bar, 0, kb * Cfg::kAtoms, b1 >> 7);
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // first CTA (its full barriers count both CTAs' bytes): the last loads
+      // issued must have landed before either CTA exits
+      if (rank == 0) {
+        const long outstanding = issued < kStages ? issued : kStages;
+        for (long i = 0; i < outstanding; ++i) {
+          if (--stage < 0) {
+            stage = kStages - 1;
+            phase ^= 1;
+          }
+          mbar_wait(&full[stage], phase, nullptr);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- issuer (first CTA)
+    if (rank == 0) {
+      constexpr int kSlotSteps = FMT == kFp4NV ? 2 : 4;  // products of 64 channels per slot
+      int stage = 0;
+      uint32_t phase = 0, slot = 0;
+      int local = 0;
+      bool ok = true;
+      for (int t = cluster; t < num_tiles && ok; t += n_clusters, ++local) {
+        if (local > 0 && !mbar_wait_warp(tempty, (uint32_t)(local - 1) & 1, abort)) {
+          if (lane == 0) *abort = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (local & 1) * kAcc1;
+        for (int kb = 0; kb < num_kb && ok; ++kb) {
+          if (!mbar_wait_warp(&full[stage], phase, abort)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a0 = smem_u32(smem) + (uint32_t)stage * Cfg::kStageBytes;
+          const uint32_t b0 = a0 + kTile, s0 = b0 + kTile;
+          const int steps = min(4, (p.K - kb * kBlockK + 63) / 64);
+#pragma unroll
+          for (int q = 0; q < 4 / kSlotSteps; ++q) {
+            if (q * kSlotSteps >= steps) break;
+            if (slot >= 2 && !mbar_wait_warp(&sfree[slot & 1], ((slot >> 1) - 1) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t cols = tmem + kScaleCol + (slot & 1) * kSlotCols;
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {  // two atoms a slot, in either format
+              const uint32_t at = s0 + (2 * q + a) * 512;
+              tmem_cp_scales_pair_w(cols + a * 12, scale_atom_desc(at));
+              tmem_cp_scales_pair_w(cols + a * 12 + 4, scale_atom_desc(at + Cfg::kScaleBytes));
+              tmem_cp_scales_pair_w(cols + a * 12 + 8, scale_atom_desc(at + 2 * Cfg::kScaleBytes));
+            }
+#pragma unroll
+            for (int i = 0; i < kSlotSteps; ++i) {
+              const int s = q * kSlotSteps + i;
+              if (s >= steps) break;
+              const int a = FMT == kFp4NV ? i : i >> 1;
+              const uint32_t id = make_idesc_fp4(256, 256, FMT == kFp4MX, FMT == kFp4MX ? (s & 1) * 2 : 0);
+              mma_fp4_ss_pair_w<FMT == kFp4NV>(d, sw128_desc(a0 + s * 32, 16), sw128_desc(b0 + s * 32, 16), id,
+                                               cols + a * 12, cols + a * 12 + 4, (kb | s) != 0);
+            }
+            mma_commit_pair_w(&sfree[slot & 1], 0x1);
+            ++slot;
+          }
+          mma_commit_pair_w(&empty[stage], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) {
+          if (lane == 0) *abort = 1;
+        } else {
+          mma_commit_pair_w(&tfull[local & 1], 0x3);
+        }
+      }
+      mma_commit_pair_w(drain, 0x3);
+      mbar_wait(drain, 0, nullptr);
+    } else if (lane == 0) {
+      // second CTA: its shared and tensor memory serve the pair's products
+      // until the last one completes
+      mbar_wait(drain, 0, nullptr);
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue (both CTAs)
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+    int local = 0;
+    for (int t = cluster; t < num_tiles; t += n_clusters, ++local) {
+      const Tile tc = pair_tile(t, tiles_m, tiles_n);
+      const int buf = local & 1;
+      if (!mbar_wait(&tfull[buf], (uint32_t)(local >> 1) & 1, abort)) {
+        if (lane == 0) *abort = 1;
+        break;
+      }
+      tc_fence_after();
+      const int64_t row = (int64_t)tc.m * 256 + rank * 128 + quad * 32 + lane;
+      const bool row_ok = row < p.M;
+      const float ra = row_ok ? __ldg(p.a_row + row) : 0.f;
+      const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * kAcc1;
+      T* out = reinterpret_cast<T*>(p.out) + row * p.ld;
+      auto release = [&]() {  // this warp has read its share of the overlapped columns
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty0);
+      };
+      if (SWIGLU) {
+        // 32-column pairs half and half + 2, those with overlapped columns first
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int c = ((i ^ buf ^ 1) ? 2 : 0) + half;
+          const int col = tc.n * 128 + c * 32;
+          uint32_t rg[32], ru[32];
+          tmem_ld32(acc + c * 32, rg);
+          tmem_ld32(acc + 128 + c * 32, ru);
+          if (i == 0) release();
+          float g[32], u[32];
+          scale_chunk(rg, ra, p.b_row + col, 32, g);
+          scale_chunk(ru, ra, p.b_row + p.N + col, 32, u);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) g[j] = g[j] / (1.f + __expf(-g[j])) * u[j];
+          if (row_ok) store_chunk(out + col, g, col, p.N);
+        }
+      } else {
+        // four 32-column chunks: one of the two with overlapped columns (6, 7
+        // of the first accumulator, 0, 1 of the second), then three others
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int c = i == 0 ? (buf ? half : 6 + half) : (buf ? 1 : -1) + 3 * half + i;
+          const int col = tc.n * 256 + c * 32;
+          uint32_t r[32];
+          tmem_ld32(acc + c * 32, r);
+          if (i == 0) release();
+          if (col >= p.N || !row_ok) continue;
+          float v[32];
+          scale_chunk(r, ra, p.b_row + col, p.N - col, v);
+          store_chunk(out + col, v, col, p.N);
+        }
+      }
+    }
+  }
+  // neither CTA leaves while the other may still signal its barriers or read
+  // its memory
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
 // ------------------------------------------------------------------ host
 bool codes_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* ptr, int64_t rows, int K,
                int box_rows) {
@@ -258,14 +566,49 @@ cudaError_t launch_few(const Fp4GemmArgs& p, const Maps& m, cudaStream_t s) {
   return p.f32 ? launch_few_t<FMT, NT, 1, float>(p, m, s) : launch_few_t<FMT, NT, 1, __nv_bfloat16>(p, m, s);
 }
 
+template <int FMT, bool SWIGLU, typename T>
+cudaError_t launch_pair_t(const Fp4GemmArgs& p, const Maps& m, int num_sms, cudaStream_t s) {
+  using Cfg = PairCfg<FMT>;
+  auto k = gemm_fp4_pair_kernel<FMT, SWIGLU, T>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (p.M + 255) / 256 * (SWIGLU ? p.N / 128 : ((int64_t)p.N + 255) / 256);
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, m.a, m.b, m.as, m.bs, p);
+}
+
+// Rows up to which the few-rows kernel runs: above them the pair kernel.
+constexpr int64_t kFewRows = 128;
+
 template <int FMT>
-cudaError_t launch_fmt(const Fp4GemmArgs& p, PFN_cuTensorMapEncodeTiled_v12000 encode, cudaStream_t s) {
+cudaError_t launch_fmt(const Fp4GemmArgs& p, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms, cudaStream_t s) {
   Maps m;
-  const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  const bool few = p.M <= kFewRows || num_sms < 2;
+  const int nt = !few ? 128 : p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   const int64_t b_rows = p.swiglu ? 2 * (int64_t)p.N : p.N;
   if (!codes_map(encode, &m.a, p.a_codes, p.M, p.K, nt) || !codes_map(encode, &m.b, p.b_codes, b_rows, p.K, 128) ||
       !scales_map(encode, &m.as, p.a_scales, p.M, p.K, FMT) || !scales_map(encode, &m.bs, p.b_scales, b_rows, p.K, FMT))
     return cudaErrorInvalidValue;
+  if (!few) {
+    if (p.swiglu)
+      return p.f32 ? launch_pair_t<FMT, true, float>(p, m, num_sms, s)
+                   : launch_pair_t<FMT, true, __nv_bfloat16>(p, m, num_sms, s);
+    return p.f32 ? launch_pair_t<FMT, false, float>(p, m, num_sms, s)
+                 : launch_pair_t<FMT, false, __nv_bfloat16>(p, m, num_sms, s);
+  }
   switch (nt) {
     case 16: return launch_few<FMT, 16>(p, m, s);
     case 32: return launch_few<FMT, 32>(p, m, s);
@@ -279,8 +622,7 @@ cudaError_t launch_fmt(const Fp4GemmArgs& p, PFN_cuTensorMapEncodeTiled_v12000 e
 cudaError_t launch_gemm_fp4(const Fp4GemmArgs& p, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms,
                             cudaStream_t s) {
   if (p.M <= 0 || p.N <= 0) return cudaSuccess;
-  (void)num_sms;
-  return p.nv ? launch_fmt<kFp4NV>(p, encode, s) : launch_fmt<kFp4MX>(p, encode, s);
+  return p.nv ? launch_fmt<kFp4NV>(p, encode, num_sms, s) : launch_fmt<kFp4MX>(p, encode, num_sms, s);
 }
 
 }  // namespace h3
