@@ -220,17 +220,21 @@ __global__ void __launch_bounds__(kFewThreads)
 // 128 gate rows and the 128 up rows that go with them.
 //
 // Tensor memory has 512 columns. Two 256-column accumulators would leave none
-// for the scales, so the second one starts at column 208, over the last 48 of
-// the first, and the scales take the 48 columns behind it. An epilogue warp
-// reads its share of the overlapped columns first and then lets the next
-// tile's products begin; the rest of its tile overlaps them.
+// for the scales, so the second one starts inside the first, and the scales
+// take the columns behind it. An epilogue warp reads its share of the
+// overlapped half into registers first and then lets the next tile's products
+// begin; the rest of its tile overlaps them.
 //
-// The scale columns are two slots of 24: 128 channels of NV scales (two
-// products), or 256 of MX scales (four). A slot is rewritten once the products
-// that read it have completed.
+// The scale columns are two slots, one per stage of 256 channels (NV 48
+// columns, MX 24). A slot is rewritten once the products that read it, those of
+// the stage before last, have completed.
+//
+// The tensor pipe takes 128 cycles a product, 512 a stage, and the issuing warp
+// has to stay below that. Copies, products and commits of a stage are one asm
+// block under one elected lane: with an election each, the issue of a stage
+// took 1000-1300 cycles (NV, 8192 x 28672 x 5376: 870 us).
 constexpr int kPairThreads = 320;  // producer, issuer, eight epilogue warps
 constexpr int kPairEpiWarps = 8;
-constexpr int kAcc1 = 208, kScaleCol = 464, kSlotCols = 24;
 constexpr int kGroupN = 12;  // tile raster: 12 N-tiles share each pass over M
 
 template <int FMT>
@@ -240,7 +244,64 @@ struct PairCfg {
   static constexpr int kStageBytes = 2 * kTile + 3 * kScaleBytes;
   static constexpr int kStages = FMT == kFp4NV ? 5 : 6;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 256;
+  static constexpr int kSlotCols = 12 * kAtoms;             // scales of A, of the two halves of B; four columns an atom
+  static constexpr int kScaleCol = 512 - 2 * kSlotCols;
+  static constexpr int kAcc1 = kScaleCol - 256;             // the second accumulator
+  static_assert(kAcc1 >= 128, "the first half of the first accumulator is not overlapped");
 };
+
+// A whole stage's tensor work for a CTA pair, issued by one lane: the scale
+// copies (atoms at sd, sd + kScaleBytes, sd + 2 kScaleBytes) to the slot at
+// column sc, the four products of 64 channels into the accumulator at column d,
+// and the commits to `sfree` (this CTA) and `empty` (both).
+#define H3_CP(T, X) "add.u32 t, %1, " #T ";\n\tadd.s64 x, %4, " #X ";\n\t" \
+                    "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], x;\n\t"
+#define H3_MM(OP, ID, SA, SB, K, P)                                                      \
+  "add.u32 t, %1, " #SA ";\n\tadd.u32 u, %1, " #SB ";\n\t"                             \
+  "add.s64 x, %2, " #K ";\n\tadd.s64 y, %3, " #K ";\n\t"                               \
+  "@e tcgen05.mma.cta_group::2." OP " [%0], x, y, " ID ", [t], [u], " P ";\n\t"
+#define H3_COMMITS                                                                                                    \
+  "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%8], %10;\n\t"         \
+  "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%9], %11;\n\t"
+#define H3_BLOCK_BEGIN                                                                 \
+  "{\n\t.reg .pred p, q, e;\n\t.reg .b32 t, u;\n\t.reg .b64 x, y;\n\t" H3_ELECT_PRED \
+  "setp.ne.b32 p, %7, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+template <int FMT>
+__device__ __forceinline__ void issue_pair_stage(uint32_t d, uint32_t sc, uint64_t ad, uint64_t bd, uint64_t sd,
+                                                 uint32_t accumulate, uint64_t* sfree, uint64_t* empty) {
+  constexpr uint32_t id0 = make_idesc_fp4(256, 256, FMT == kFp4MX, 0), id1 = make_idesc_fp4(256, 256, FMT == kFp4MX, 2);
+#define H3_ARGS                                                                                             \
+  ::"r"(d), "r"(sc), "l"(ad), "l"(bd), "l"(sd), "r"(id0), "r"(id1), "r"(accumulate), "r"(smem_u32(sfree)),  \
+      "r"(smem_u32(empty)), "h"((uint16_t)1), "h"((uint16_t)3)                                             \
+      : "memory"
+  if (FMT == kFp4NV) {
+#define H3_NV "kind::mxf4nvf4.block_scale.scale_vec::4X"
+    static_assert(PairCfg<kFp4NV>::kScaleBytes == 128 * 16 && PairCfg<kFp4MX>::kScaleBytes == 64 * 16, "offsets below");
+    asm volatile(H3_BLOCK_BEGIN                                                      //
+                 H3_CP(0, 0) H3_CP(4, 128) H3_CP(8, 256)                             //
+                 H3_MM(H3_NV, "%5", 0, 4, 0, "p")                                    //
+                 H3_CP(12, 32) H3_CP(16, 160) H3_CP(20, 288)                         //
+                 H3_MM(H3_NV, "%5", 12, 16, 2, "q")                                  //
+                 H3_CP(24, 64) H3_CP(28, 192) H3_CP(32, 320)                         //
+                 H3_MM(H3_NV, "%5", 24, 28, 4, "q")                                  //
+                 H3_CP(36, 96) H3_CP(40, 224) H3_CP(44, 352)                         //
+                 H3_MM(H3_NV, "%5", 36, 40, 6, "q") H3_COMMITS "}" H3_ARGS);
+#undef H3_NV
+  } else {
+#define H3_MX "kind::mxf4.block_scale.scale_vec::2X"
+    asm volatile(H3_BLOCK_BEGIN                                                      //
+                 H3_CP(0, 0) H3_CP(4, 64) H3_CP(8, 128)                              //
+                 H3_MM(H3_MX, "%5", 0, 4, 0, "p") H3_MM(H3_MX, "%6", 0, 4, 2, "q")   //
+                 H3_CP(12, 32) H3_CP(16, 96) H3_CP(20, 160)                          //
+                 H3_MM(H3_MX, "%5", 12, 16, 4, "q") H3_MM(H3_MX, "%6", 12, 16, 6, "q") H3_COMMITS "}" H3_ARGS);
+#undef H3_MX
+  }
+#undef H3_ARGS
+}
+#undef H3_CP
+#undef H3_MM
+#undef H3_COMMITS
+#undef H3_BLOCK_BEGIN
 
 struct Tile {
   int m, n;
@@ -271,7 +332,7 @@ __device__ __forceinline__ void store_chunk(T* dst, const float (&v)[32], int co
 }
 // Accumulators times the row scales of A's row and of 32 weight rows from `rb`
 // (of which those past `left` are absent).
-__device__ __forceinline__ void scale_chunk(const uint32_t (&r)[32], float ra, const float* rb, int left, float (&v)[32]) {
+__device__ __forceinline__ void scale_chunk(const uint32_t* r, float ra, const float* rb, int left, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float4 b = 4 * i < left ? __ldg(reinterpret_cast<const float4*>(rb) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -336,7 +397,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers are initialised and their tensor memory allocated
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // all 512 columns are this CTA's, so they start at address 0: a constant
+  // that the issue loop need not carry (checked all the same)
+  if (*tmem_slot != 0) *abort = 1;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer (both CTAs)
@@ -387,9 +450,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- issuer (first CTA)
     if (rank == 0) {
-      constexpr int kSlotSteps = FMT == kFp4NV ? 2 : 4;  // products of 64 channels per slot
       int stage = 0;
-      uint32_t phase = 0, slot = 0;
+      uint32_t phase = 0, slot = 0;  // slot: stages issued so far
       int local = 0;
       bool ok = true;
       for (int t = cluster; t < num_tiles && ok; t += n_clusters, ++local) {
@@ -398,44 +460,40 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + (local & 1) * kAcc1;
-        for (int kb = 0; kb < num_kb && ok; ++kb) {
-          if (!mbar_wait_warp(&full[stage], phase, abort)) {
+        const uint32_t d = (local & 1) * Cfg::kAcc1;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait_warp(&full[stage], phase, abort) ||
+              (slot >= 2 && !mbar_wait_warp(&sfree[slot & 1], ((slot >> 1) - 1) & 1, abort))) {
             ok = false;
             break;
           }
+          tc_fence_after();
           const uint32_t a0 = smem_u32(smem) + (uint32_t)stage * Cfg::kStageBytes;
           const uint32_t b0 = a0 + kTile, s0 = b0 + kTile;
-          const int steps = min(4, (p.K - kb * kBlockK + 63) / 64);
-#pragma unroll
-          for (int q = 0; q < 4 / kSlotSteps; ++q) {
-            if (q * kSlotSteps >= steps) break;
-            if (slot >= 2 && !mbar_wait_warp(&sfree[slot & 1], ((slot >> 1) - 1) & 1, abort)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t cols = tmem + kScaleCol + (slot & 1) * kSlotCols;
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {  // two atoms a slot, in either format
-              const uint32_t at = s0 + (2 * q + a) * 512;
-              tmem_cp_scales_pair_w(cols + a * 12, scale_atom_desc(at));
-              tmem_cp_scales_pair_w(cols + a * 12 + 4, scale_atom_desc(at + Cfg::kScaleBytes));
-              tmem_cp_scales_pair_w(cols + a * 12 + 8, scale_atom_desc(at + 2 * Cfg::kScaleBytes));
-            }
-#pragma unroll
-            for (int i = 0; i < kSlotSteps; ++i) {
-              const int s = q * kSlotSteps + i;
-              if (s >= steps) break;
-              const int a = FMT == kFp4NV ? i : i >> 1;
+          const uint32_t cols = Cfg::kScaleCol + (slot & 1) * Cfg::kSlotCols;
+          const int left = p.K - kb * kBlockK;
+          if (left > kBlockK - 64) {
+            issue_pair_stage<FMT>(d, cols, sw128_desc(a0, 16), sw128_desc(b0, 16), scale_atom_desc(s0), kb != 0,
+                                  &sfree[slot & 1], &empty[stage]);
+          } else {  // the last stage of a K that does not fill it
+            const int steps = (left + 63) / 64;
+#pragma unroll 1
+            for (int s = 0; s < steps; ++s) {
+              const int a = s * 64 / fp4_atom_channels(FMT);
+              const uint32_t col = cols + a * 12, at = s0 + a * 512;
+              if (s * 64 % fp4_atom_channels(FMT) == 0) {
+                tmem_cp_scales_pair_w(col, scale_atom_desc(at));
+                tmem_cp_scales_pair_w(col + 4, scale_atom_desc(at + Cfg::kScaleBytes));
+                tmem_cp_scales_pair_w(col + 8, scale_atom_desc(at + 2 * Cfg::kScaleBytes));
+              }
               const uint32_t id = make_idesc_fp4(256, 256, FMT == kFp4MX, FMT == kFp4MX ? (s & 1) * 2 : 0);
-              mma_fp4_ss_pair_w<FMT == kFp4NV>(d, sw128_desc(a0 + s * 32, 16), sw128_desc(b0 + s * 32, 16), id,
-                                               cols + a * 12, cols + a * 12 + 4, (kb | s) != 0);
+              mma_fp4_ss_pair_w<FMT == kFp4NV>(d, sw128_desc(a0 + s * 32, 16), sw128_desc(b0 + s * 32, 16), id, col,
+                                               col + 4, (kb | s) != 0);
             }
             mma_commit_pair_w(&sfree[slot & 1], 0x1);
-            ++slot;
+            mma_commit_pair_w(&empty[stage], 0x3);
           }
-          mma_commit_pair_w(&empty[stage], 0x3);
+          ++slot;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
@@ -470,45 +528,45 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int64_t row = (int64_t)tc.m * 256 + rank * 128 + quad * 32 + lane;
       const bool row_ok = row < p.M;
       const float ra = row_ok ? __ldg(p.a_row + row) : 0.f;
-      const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * kAcc1;
+      const uint32_t acc = ((uint32_t)(quad * 32) << 16) + buf * Cfg::kAcc1 + half * 64;
       T* out = reinterpret_cast<T*>(p.out) + row * p.ld;
-      auto release = [&]() {  // this warp has read its share of the overlapped columns
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty0);
-      };
-      if (SWIGLU) {
-        // 32-column pairs half and half + 2, those with overlapped columns first
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          const int c = ((i ^ buf ^ 1) ? 2 : 0) + half;
-          const int col = tc.n * 128 + c * 32;
-          uint32_t rg[32], ru[32];
-          tmem_ld32(acc + c * 32, rg);
-          tmem_ld32(acc + 128 + c * 32, ru);
-          if (i == 0) release();
-          float g[32], u[32];
-          scale_chunk(rg, ra, p.b_row + col, 32, g);
-          scale_chunk(ru, ra, p.b_row + p.N + col, 32, u);
+      // this warp's 64 columns of the tile's half that the other accumulator
+      // overlaps (the first one's upper, the second one's lower), then the
+      // next tile's products may begin
+      uint32_t f[64];
+      tmem_ld64(acc + (buf ? 0 : 128), f);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty0);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) g[j] = g[j] / (1.f + __expf(-g[j])) * u[j];
+      for (int q = 0; q < 2; ++q) {
+        uint32_t r[32];
+        tmem_ld32(acc + (buf ? 128 : 0) + q * 32, r);
+        if (SWIGLU) {
+          const int col = tc.n * 128 + half * 64 + q * 32;
+          float g[32], u[32];
+          scale_chunk(f + 32 * q, ra, p.b_row + (buf ? col : p.N + col), 32, g);
+          scale_chunk(r, ra, p.b_row + (buf ? p.N + col : col), 32, u);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float gate = buf ? g[j] : u[j], up = buf ? u[j] : g[j];
+            g[j] = gate / (1.f + __expf(-gate)) * up;
+          }
           if (row_ok) store_chunk(out + col, g, col, p.N);
-        }
-      } else {
-        // four 32-column chunks: one of the two with overlapped columns (6, 7
-        // of the first accumulator, 0, 1 of the second), then three others
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const int c = i == 0 ? (buf ? half : 6 + half) : (buf ? 1 : -1) + 3 * half + i;
-          const int col = tc.n * 256 + c * 32;
-          uint32_t r[32];
-          tmem_ld32(acc + c * 32, r);
-          if (i == 0) release();
-          if (col >= p.N || !row_ok) continue;
+        } else {
+          const int col = tc.n * 256 + half * 64 + q * 32;
+          const int c0 = col + (buf ? 0 : 128), c1 = col + (buf ? 128 : 0);
           float v[32];
-          scale_chunk(r, ra, p.b_row + col, p.N - col, v);
-          store_chunk(out + col, v, col, p.N);
+          if (row_ok && c0 < p.N) {
+            scale_chunk(f + 32 * q, ra, p.b_row + c0, p.N - c0, v);
+            store_chunk(out + c0, v, c0, p.N);
+          }
+          if (row_ok && c1 < p.N) {
+            scale_chunk(r, ra, p.b_row + c1, p.N - c1, v);
+            store_chunk(out + c1, v, c1, p.N);
+          }
         }
+        __syncwarp();
       }
     }
   }
@@ -517,7 +575,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (warp == 1) tmem_dealloc_pair(*tmem_slot, 512);
 }
 
 // ------------------------------------------------------------------ host
