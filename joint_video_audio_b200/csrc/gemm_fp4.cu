@@ -30,6 +30,10 @@ constexpr int kTile = 128 * kRowBytes;
 
 __host__ __device__ constexpr int atoms_per_stage(int fmt) { return kBlockK / fp4_atom_channels(fmt); }
 
+// silu(g) * u; the approximate quotient is off by a few units of the last
+// place (and 0 where the denominator overflows, as the exact one rounds).
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
 // ------------------------------------------------------------------ few rows
 constexpr int kFewThreads = 192;
 
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(kFewThreads)
           if (m < p.M && n_ok) {
             const float ra = __ldg(p.a_row + m);
             float v = __uint_as_float(g[i]) * ra * rb;
-            if (NW == 2) v = v / (1.f + __expf(-v)) * (__uint_as_float(u[i]) * ra * ru);
+            if (NW == 2) v = swiglu(v, __uint_as_float(u[i]) * ra * ru);
             if (sizeof(T) == 2)
               reinterpret_cast<__nv_bfloat16*>(p.out)[m * p.ld + n] = __float2bfloat16_rn(v);
             else
@@ -242,8 +246,10 @@ struct PairCfg {
   static constexpr int kAtoms = atoms_per_stage(FMT);
   static constexpr int kScaleBytes = kAtoms * 512;  // of 128 rows
   static constexpr int kStageBytes = 2 * kTile + 3 * kScaleBytes;
-  static constexpr int kStages = FMT == kFp4NV ? 5 : 6;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 256;
+  static constexpr int kStages = 5;
+  static constexpr size_t kSlack = 768;  // to align the base to 1024 bytes
+  static constexpr size_t kSmem = kSlack + (size_t)kStages * kStageBytes + kPairEpiWarps * (32 * 128 + 512) + 144;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
   static constexpr int kSlotCols = 12 * kAtoms;             // scales of A, of the two halves of B; four columns an atom
   static constexpr int kScaleCol = 512 - 2 * kSlotCols;
   static constexpr int kAcc1 = kScaleCol - 256;             // the second accumulator
@@ -314,46 +320,76 @@ __device__ __forceinline__ Tile pair_tile(int t, int tiles_m, int tiles_n) {
   return {i / gn, first + i % gn};
 }
 
-// One row's 32 columns from `col`, as far as N reaches (a multiple of 8).
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* dst, const float (&v)[32], int col, int N) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (col + 8 * i >= N) break;
-    if (sizeof(T) == 2) {
-      reinterpret_cast<uint4*>(dst)[i] =
-          make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                     pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-    } else {
-      reinterpret_cast<float4*>(dst)[2 * i] = make_float4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
-      reinterpret_cast<float4*>(dst)[2 * i + 1] = make_float4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
-    }
-  }
+// Output goes through shared memory, one unit of 32 rows x 128 bytes per
+// epilogue warp at a time, and leaves by a TMA store that also clips it at the
+// matrix's edges. Storing 16 bytes a lane from the accumulators' row-per-lane
+// layout, with the scales read from global memory behind the products, an
+// epilogue took 13,000 cycles a tile, more than the 11,000 of the products at
+// K = 5376.
+constexpr int kUnitBytes = 32 * 128;
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
 }
-// Accumulators times the row scales of A's row and of 32 weight rows from `rb`
-// (of which those past `left` are absent).
-__device__ __forceinline__ void scale_chunk(const uint32_t* r, float ra, const float* rb, int left, float (&v)[32]) {
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// One epilogue warp's unit: lane's row of v, as T, to the unit with the
+// 128-byte swizzle, then stored at column x, row y where that lies inside.
+template <typename T>
+__device__ __forceinline__ void store_unit(uint8_t* unit, const CUtensorMap* m, int lane, const float* v, int x, int64_t y,
+                                           const Fp4GemmArgs& p) {
+  if (lane == 0) bulk_wait_read();  // the unit's last store has read it
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float4 b = 4 * i < left ? __ldg(reinterpret_cast<const float4*>(rb) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    uint4 o;
+    if (sizeof(T) == 2)
+      o = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                     pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    else
+      o = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                     __float_as_uint(v[4 * i + 3]));
+    *reinterpret_cast<uint4*>(unit + lane * 128 + ((i ^ (lane & 7)) << 4)) = o;
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (x < p.N && y < p.M) tma_store_2d(m, unit, x, (int)y);
+    bulk_commit();
+  }
+}
+// 32 accumulators of a lane's row times its row scale and the 32 weight rows'.
+__device__ __forceinline__ void scale_chunk(const uint32_t* r, float ra, const float* rb, float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 b = reinterpret_cast<const float4*>(rb)[i];
     v[4 * i] = __uint_as_float(r[4 * i]) * ra * b.x;
     v[4 * i + 1] = __uint_as_float(r[4 * i + 1]) * ra * b.y;
     v[4 * i + 2] = __uint_as_float(r[4 * i + 2]) * ra * b.z;
     v[4 * i + 3] = __uint_as_float(r[4 * i + 3]) * ra * b.w;
   }
 }
-
 template <int FMT, bool SWIGLU, typename T>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmAS, const __grid_constant__ CUtensorMap tmBS,
-                         const Fp4GemmArgs p) {
+                         const __grid_constant__ CUtensorMap tmOut, const Fp4GemmArgs p) {
   using Cfg = PairCfg<FMT>;
   constexpr int kStages = Cfg::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-  // stage: A tile, B tile, A scales, scales of the tile's first and second 128 weight rows
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)kStages * Cfg::kStageBytes);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // (the declared alignment makes this 0; an early return instead of the
+  // bound costs the issuing warp a fifth of its speed)
+  uint8_t* smem = smem_raw + min(((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw), (uint32_t)Cfg::kSlack);
+  // stages (A tile, B tile, A scales, scales of the tile's first and second
+  // 128 weight rows), the warps' output units, their row scales, the barriers
+  uint8_t* units = smem + (size_t)kStages * Cfg::kStageBytes;
+  float* rbs = reinterpret_cast<float*>(units + kPairEpiWarps * kUnitBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(rbs + kPairEpiWarps * 128);
   uint64_t* empty = full + kStages;
   uint64_t* sfree = empty + kStages;
   uint64_t* tfull = sfree + 2;
@@ -462,8 +498,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t d = (local & 1) * Cfg::kAcc1;
         for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait_warp(&full[stage], phase, abort) ||
-              (slot >= 2 && !mbar_wait_warp(&sfree[slot & 1], ((slot >> 1) - 1) & 1, abort))) {
+          const bool ready = (slot < 2 || mbar_wait(&sfree[slot & 1], ((slot >> 1) - 1) & 1, abort)) &&
+                             mbar_wait(&full[stage], phase, abort);
+          if (!__all_sync(0xffffffffu, ready)) {
             ok = false;
             break;
           }
@@ -516,59 +553,67 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+    uint8_t* unit = units + (warp - 2) * kUnitBytes;
+    float* rb = rbs + (warp - 2) * 128;
     int local = 0;
     for (int t = cluster; t < num_tiles; t += n_clusters, ++local) {
       const Tile tc = pair_tile(t, tiles_m, tiles_n);
       const int buf = local & 1;
+      const int64_t row0 = (int64_t)tc.m * 256 + rank * 128 + quad * 32;
+      // the warp's 64 columns of each half of the tile; their weight rows' scales,
+      // and the lane's own, are fetched while the products run
+      const int col0 = SWIGLU ? tc.n * 128 + half * 64 : tc.n * 256 + half * 64;
+      const int row_b = col0 + (lane >> 4) * (SWIGLU ? p.N : 128) + (lane & 15) * 4;
+      const int rows_b = SWIGLU ? 2 * p.N : p.N;
+      __syncwarp();  // the last tile's scales have been read
+      reinterpret_cast<float4*>(rb)[lane] =
+          row_b < rows_b ? __ldg(reinterpret_cast<const float4*>(p.b_row + row_b)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float ra = row0 + lane < p.M ? __ldg(p.a_row + row0 + lane) : 0.f;
+      __syncwarp();
       if (!mbar_wait(&tfull[buf], (uint32_t)(local >> 1) & 1, abort)) {
         if (lane == 0) *abort = 1;
         break;
       }
       tc_fence_after();
-      const int64_t row = (int64_t)tc.m * 256 + rank * 128 + quad * 32 + lane;
-      const bool row_ok = row < p.M;
-      const float ra = row_ok ? __ldg(p.a_row + row) : 0.f;
       const uint32_t acc = ((uint32_t)(quad * 32) << 16) + buf * Cfg::kAcc1 + half * 64;
-      T* out = reinterpret_cast<T*>(p.out) + row * p.ld;
-      // this warp's 64 columns of the tile's half that the other accumulator
+      // this warp's columns of the tile's half that the other accumulator
       // overlaps (the first one's upper, the second one's lower), then the
       // next tile's products may begin
       uint32_t f[64];
       tmem_ld64(acc + (buf ? 0 : 128), f);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty0);
+      if (lane == 0) mbar_arrive_cluster_relaxed(tempty0);
+      constexpr int kUnitCols = 128 / (int)sizeof(T);
+      float v[64];
+      if (SWIGLU) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t r[32];
-        tmem_ld32(acc + (buf ? 128 : 0) + q * 32, r);
-        if (SWIGLU) {
-          const int col = tc.n * 128 + half * 64 + q * 32;
+        for (int q = 0; q < 2; ++q) {
+          uint32_t r[32];
+          tmem_ld32(acc + (buf ? 128 : 0) + q * 32, r);
           float g[32], u[32];
-          scale_chunk(f + 32 * q, ra, p.b_row + (buf ? col : p.N + col), 32, g);
-          scale_chunk(r, ra, p.b_row + (buf ? p.N + col : col), 32, u);
+          scale_chunk(buf ? f + 32 * q : r, ra, rb + q * 32, g);
+          scale_chunk(buf ? r : f + 32 * q, ra, rb + 64 + q * 32, u);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float gate = buf ? g[j] : u[j], up = buf ? u[j] : g[j];
-            g[j] = gate / (1.f + __expf(-gate)) * up;
-          }
-          if (row_ok) store_chunk(out + col, g, col, p.N);
-        } else {
-          const int col = tc.n * 256 + half * 64 + q * 32;
-          const int c0 = col + (buf ? 0 : 128), c1 = col + (buf ? 128 : 0);
-          float v[32];
-          if (row_ok && c0 < p.N) {
-            scale_chunk(f + 32 * q, ra, p.b_row + c0, p.N - c0, v);
-            store_chunk(out + c0, v, c0, p.N);
-          }
-          if (row_ok && c1 < p.N) {
-            scale_chunk(r, ra, p.b_row + c1, p.N - c1, v);
-            store_chunk(out + c1, v, c1, p.N);
-          }
+          for (int i = 0; i < 32; ++i) v[32 * q + i] = swiglu(g[i], u[i]);
+          if (kUnitCols == 32) store_unit<T>(unit, &tmOut, lane, v + 32 * q, col0 + 32 * q, row0, p);
         }
-        __syncwarp();
+        if (kUnitCols == 64) store_unit<T>(unit, &tmOut, lane, v, col0, row0, p);
+      } else {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int h1 = hf ? buf : 1 - buf;  // which half of the tile: the overlapped one first
+          if (hf) tmem_ld64(acc + (buf ? 128 : 0), f);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            scale_chunk(f + 32 * q, ra, rb + h1 * 64 + q * 32, v + 32 * q);
+            if (kUnitCols == 32) store_unit<T>(unit, &tmOut, lane, v + 32 * q, col0 + h1 * 128 + 32 * q, row0, p);
+          }
+          if (kUnitCols == 64) store_unit<T>(unit, &tmOut, lane, v, col0 + h1 * 128, row0, p);
+        }
       }
     }
+    if (lane == 0) bulk_wait();  // the output has left shared memory and reached the matrix
   }
   // neither CTA leaves while the other may still signal its barriers or read
   // its memory
@@ -602,8 +647,20 @@ bool scales_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The output, stored in units of 32 rows x 128 bytes.
+bool out_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const Fp4GemmArgs& p) {
+  const cuuint64_t es = p.f32 ? 4 : 2;
+  cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
+  cuuint64_t strides[1] = {(cuuint64_t)p.ld * es};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(m, p.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, dims, strides,
+                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Maps {
-  CUtensorMap a, b, as, bs;
+  CUtensorMap a, b, as, bs, out;
 };
 
 template <int FMT, int NT, int NW, typename T>
@@ -645,7 +702,7 @@ cudaError_t launch_pair_t(const Fp4GemmArgs& p, const Maps& m, int num_sms, cuda
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, m.a, m.b, m.as, m.bs, p);
+  return cudaLaunchKernelEx(&cfg, k, m.a, m.b, m.as, m.bs, m.out, p);
 }
 
 // Rows up to which the few-rows kernel runs: above them the pair kernel.
@@ -661,6 +718,7 @@ cudaError_t launch_fmt(const Fp4GemmArgs& p, PFN_cuTensorMapEncodeTiled_v12000 e
       !scales_map(encode, &m.as, p.a_scales, p.M, p.K, FMT) || !scales_map(encode, &m.bs, p.b_scales, b_rows, p.K, FMT))
     return cudaErrorInvalidValue;
   if (!few) {
+    if (!out_map(encode, &m.out, p)) return cudaErrorInvalidValue;
     if (p.swiglu)
       return p.f32 ? launch_pair_t<FMT, true, float>(p, m, num_sms, s)
                    : launch_pair_t<FMT, true, __nv_bfloat16>(p, m, num_sms, s);

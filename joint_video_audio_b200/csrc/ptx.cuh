@@ -155,6 +155,13 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same without release semantics, for an arrival that hands over tensor
+// memory whose reads have completed (tcgen05.wait::ld) and nothing else. The
+// release form also waits for the thread's outstanding global accesses:
+// ~1500 cycles in an epilogue.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // 2-D tiled load into this CTA's shared memory for a CTA-pair product; the
 // transaction bytes are signalled on the mbarrier at `bar_cluster` (a
 // cluster-window address, here always the pair's first CTA).
