@@ -160,28 +160,34 @@ __device__ __forceinline__ void chunk_amax(const float (&h)[32], float (&am)[4])
   }
 }
 
+// Eight values of an MX block with largest magnitude `amax` -> codes and the
+// block's scale byte. The scale is the smallest 2^e with amax <= 7 * 2^e: an
+// amax in (6, 7] takes the code 6 under 2^e and under 2^(e+1) alike, so the
+// smaller scale is never the worse one. Multiplying by 2^-e is exact, hence so
+// are the codes. A block with a non-finite value gets the NaN scale.
+__device__ __forceinline__ uint32_t quant8_mx(float* h, float amax, uint32_t& scale) {
+  const uint32_t bits = __float_as_uint(amax) & 0x7fffffffu;
+  int code = (int)(bits >> 23) - 2 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  code = code < 1 ? 1 : code;
+  const bool ok = bits < 0x7f800000u;
+  const float inv = __uint_as_float((uint32_t)(ok ? 254 - code : 0) << 23);
+  scale = (uint32_t)(ok ? code : 255);
+  const uint64_t inv2 = f2_pack(inv, inv);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) f2_unpack(f2_mul(f2_pack(h[e], h[e + 1]), inv2), h[e], h[e + 1]);
+  return e2m1x8(h);
+}
 // MX: am[j] of the lane's chunks -> the group's codes and its four scale bytes
-// (the same word in every lane). The scale is the smallest 2^e with
-// amax <= 7 * 2^e: an amax in (6, 7] takes the code 6 under 2^e and under
-// 2^(e+1) alike, so the smaller scale is never the worse one. Multiplying by
-// 2^-e is exact, hence so are the codes. A block with a non-finite value gets
-// the NaN scale.
+// (the same word in every lane).
 __device__ __forceinline__ void quant_mx(float (&h)[32], float (&am)[4], uint32_t (&codes)[4], uint32_t& scale_word) {
   scale_word = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     am[j] = max_nan(am[j], __shfl_xor_sync(0xffffffffu, am[j], 1));
     am[j] = max_nan(am[j], __shfl_xor_sync(0xffffffffu, am[j], 2));
-    const uint32_t bits = __float_as_uint(am[j]) & 0x7fffffffu;
-    int code = (int)(bits >> 23) - 2 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    code = code < 1 ? 1 : code;
-    const bool ok = bits < 0x7f800000u;
-    const float inv = __uint_as_float((uint32_t)(ok ? 254 - code : 0) << 23);
-    scale_word |= (uint32_t)(ok ? code : 255) << (8 * j);
-    const uint64_t inv2 = f2_pack(inv, inv);
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) f2_unpack(f2_mul(f2_pack(h[8 * j + e], h[8 * j + e + 1]), inv2), h[8 * j + e], h[8 * j + e + 1]);
-    codes[j] = e2m1x8(h + 8 * j);
+    uint32_t sc;
+    codes[j] = quant8_mx(h + 8 * j, am[j], sc);
+    scale_word |= sc << (8 * j);
   }
 }
 
@@ -204,31 +210,37 @@ __device__ __forceinline__ int nv_row_exponent(float amax) {
   const int e = (int)(bits >> 23) - 127 - 11 + ((bits & 0x7fffffu) > 0x280000u ? 1 : 0);  // 2688 = 1.3125 * 2^11
   return e < -126 ? -126 : e;
 }
-// NV, second half: codes and the lane's four scale bytes, one per chunk (byte
-// j: block 2 j + l / 2 of the 128 channels). The block scale is amax / 6 in
-// e4m3; the quotient u / s is rounded correctly (one Newton step with the exact
+// Eight values of an NV block with largest magnitude `amax`, in a row of scale
+// 1 / inv_row -> codes and the block's scale byte, amax / 6 in e4m3. The
+// quotient u / s is rounded correctly (one Newton step with the exact
 // remainder), so a value halfway between two codes is seen as such. It is
 // taken as -u / s, whose steps keep the sign of a zero, and the codes' signs
 // are flipped at the end.
+__device__ __forceinline__ uint32_t quant8_nv(float* h, float amax, float inv_row, uint32_t& scale) {
+  const bool ok = finite_bits(amax);
+  scale = ok ? e4m3_code(__fdiv_rn(amax * inv_row, 6.f)) : 0x7fu;
+  const float s = ok ? e4m3_value(scale) : 0.f;
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  const uint64_t inv2 = f2_pack(inv_row, inv_row), nr2 = f2_pack(-r, -r), s2 = f2_pack(s, s);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const uint64_t u = f2_mul(f2_pack(h[e], h[e + 1]), inv2);
+    const uint64_t nq = f2_mul(u, nr2);
+    f2_unpack(f2_fma(f2_fma(nq, s2, u), nr2, nq), h[e], h[e + 1]);
+  }
+  return e2m1x8(h) ^ 0x88888888u;
+}
+__device__ __forceinline__ float pow2_float(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// NV, second half: codes and the lane's four scale bytes, one per chunk (byte
+// j: block 2 j + l / 2 of the 128 channels).
 __device__ __forceinline__ void quant_nv(float (&h)[32], const float (&am)[4], int row_exp, uint32_t (&codes)[4],
                                          uint32_t& scale_bytes) {
-  const float inv_row = __uint_as_float((uint32_t)(127 - row_exp) << 23);
   scale_bytes = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const bool ok = finite_bits(am[j]);
-    const uint32_t code = ok ? e4m3_code(__fdiv_rn(am[j] * inv_row, 6.f)) : 0x7fu;
-    const float s = ok ? e4m3_value(code) : 0.f;
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-    scale_bytes |= code << (8 * j);
-    const uint64_t inv2 = f2_pack(inv_row, inv_row), nr2 = f2_pack(-r, -r), s2 = f2_pack(s, s);
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const uint64_t u = f2_mul(f2_pack(h[8 * j + e], h[8 * j + e + 1]), inv2);
-      const uint64_t nq = f2_mul(u, nr2);
-      f2_unpack(f2_fma(f2_fma(nq, s2, u), nr2, nq), h[8 * j + e], h[8 * j + e + 1]);
-    }
-    codes[j] = e2m1x8(h + 8 * j) ^ 0x88888888u;
+    uint32_t sc;
+    codes[j] = quant8_nv(h + 8 * j, am[j], pow2_float(-row_exp), sc);
+    scale_bytes |= sc << (8 * j);
   }
 }
 

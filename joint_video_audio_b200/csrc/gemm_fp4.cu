@@ -498,9 +498,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t d = (local & 1) * Cfg::kAcc1;
         for (int kb = 0; kb < num_kb; ++kb) {
-          const bool ready = (slot < 2 || mbar_wait(&sfree[slot & 1], ((slot >> 1) - 1) & 1, abort)) &&
-                             mbar_wait(&full[stage], phase, abort);
-          if (!__all_sync(0xffffffffu, ready)) {
+          // both barriers are looked at once before either is waited for; a slot's
+          // first use finds its barrier's preceding phase, which counts as complete
+          const uint32_t sfree_parity = ((slot >> 1) & 1) ^ 1;
+          const bool r0 = mbar_try_wait(&full[stage], phase), r1 = mbar_try_wait(&sfree[slot & 1], sfree_parity);
+          if (!__all_sync(0xffffffffu, r0 && r1) &&
+              !(mbar_wait_warp(&full[stage], phase, abort) && mbar_wait_warp(&sfree[slot & 1], sfree_parity, abort))) {
             ok = false;
             break;
           }

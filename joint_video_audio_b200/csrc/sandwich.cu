@@ -10,9 +10,12 @@
 // fewer than a pass over the stored x1) and leaves as bf16 or as the 4-bit
 // operand of the next product, quantised from its fp32 values (fp4.cuh).
 //
-// Bound by moving x, y, x1 and h once: 8 bytes a value (6.5 with a 4-bit h). A
-// row is spread over whole warps and lives in registers across its two or
-// three reductions.
+// Bound by moving x, y, x1 and h once: 8 bytes a value (6.5 with a 4-bit h),
+// against 14 bytes a value of gate, gain, shift and scale if each row read
+// them. So a persistent CTA takes a contiguous slice of the rows, visits them
+// grouped by (tag, tidx), and a thread keeps its eight channels' vectors in
+// registers while the key stays. Rows arrive by bulk copies issued several
+// rows ahead; a row's two or three reductions are one barrier each.
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"
@@ -21,26 +24,14 @@
 namespace h3 {
 namespace {
 
-constexpr int kMaxRowWarps = 16;
-constexpr int kSmallCta = 8;
+constexpr int kMaxStages = 8;
+constexpr int kSortRows = 256;  // rows grouped by key at a time
 
-// Sum (IS_MAX: max of non-negative values) over the row's warps.
-template <bool IS_MAX>
-__device__ __forceinline__ float row_reduce(float v, float* red, int warp, int w, int warps) {
-  if (IS_MAX) {
-    v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
-  } else {
-#pragma unroll
-    for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  }
-  if (warps == 1) return v;
-  if ((threadIdx.x & 31) == 0) red[warp] = v;
-  __syncthreads();
-  float r = red[warp - w];
-  for (int i = 1; i < warps; ++i) r = IS_MAX ? fmaxf(r, red[warp - w + i]) : r + red[warp - w + i];
-  return r;
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
-
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -49,128 +40,287 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// HOUT: 0 no h, 1 bf16, 2 MX, 3 NV.
-template <int HOUT, bool ROT>
-__global__ void __launch_bounds__(kMaxRowWarps * 32) sandwich_kernel(const SandwichArgs a, int warps, int katoms) {
-  __shared__ float red[3][kMaxRowWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_cta = (blockDim.x >> 5) / warps;
-  const int64_t row = (int64_t)blockIdx.x * per_cta + warp / warps;
-  const int w = warp % warps;
-  const int blk = w * 8 + (lane >> 2), l = lane & 3;
-  const bool ok = row < a.rows && blk * 128 < a.C;  // C is a multiple of 128: a group is all in or all out
-  const float *gate = nullptr, *mod = nullptr;
-  if (row < a.rows) {
-    const int tg = a.tag[row], ti = a.tidx[row];
-    if (tg >= 0 && tg < a.n_tags && ti >= 0 && ti < a.n_t) {
-      const int64_t key = ((int64_t)tg * a.n_t + ti) * 6;
-      gate = a.table + (key + a.gate_idx) * a.C;
-      if (HOUT) mod = a.norm_table + (key + a.shift_idx) * a.C;  // shift, then scale
-    }
-  }
-  const int64_t base = row * a.C + blk * 128 + l * 8;
-  float x[32], y[32];
+// Sum (IS_MAX: max of non-negative values) over the CTA; one barrier. `red`
+// has a slot per warp, of 32, those past the last warp zero, and is written
+// again after another barrier at least.
+template <bool IS_MAX>
+__device__ __forceinline__ float warp_reduce(float v) {
+  if (IS_MAX) return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint4 xv = make_uint4(0, 0, 0, 0), yv = xv;
-    if (ok) {
-      xv = *reinterpret_cast<const uint4*>(a.x + base + 32 * j);
-      yv = *reinterpret_cast<const uint4*>(a.y + base + 32 * j);
-    }
-    unpack_bf16x8(xv, x + 8 * j);
-    unpack_bf16x8(yv, y + 8 * j);
-  }
-  float rp = a.branch_scale;
-  if (a.post_norm) {
-    float ss = 0.f;
+  for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+template <bool IS_MAX>
+__device__ __forceinline__ float cta_reduce(float v, float* red) {
+  v = warp_reduce<IS_MAX>(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_reduce<IS_MAX>(red[threadIdx.x & 31]);
+}
+// Sum of the squares of eight values.
+__device__ __forceinline__ float squares8(const float (&v)[8]) {
+  uint64_t s2 = f2_mul(f2_pack(v[0], v[1]), f2_pack(v[0], v[1]));
 #pragma unroll
-    for (int e = 0; e < 32; ++e) ss = fmaf(y[e], y[e], ss);
-    rp *= rsqrtf(row_reduce<false>(ss, red[0], warp, w, warps) / (float)a.C + a.post_eps);
-  }
-  if (ok) {
+  for (int e = 2; e < 8; e += 2) s2 = f2_fma(f2_pack(v[e], v[e + 1]), f2_pack(v[e], v[e + 1]), s2);
+  float a, b;
+  f2_unpack(s2, a, b);
+  return a + b;
+}
+// v[e] = a[e] * s * b[e] + c[e]
+__device__ __forceinline__ void scale_fma8(float (&v)[8], const float (&a)[8], float s, const float (&b)[8],
+                                           const float (&c)[8]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = blk * 128 + j * 32 + l * 8;
-      if (gate) {
-        float g[8];
-        load8(gate + c, g);
-        if (a.post_gain) {
-          float pg[8];
-          unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(a.post_gain + c)), pg);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] *= pg[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[8 * j + e] = fmaf(g[e] * rp, y[8 * j + e], x[8 * j + e]);
-      }
-      *reinterpret_cast<uint4*>(a.x_out + base + 32 * j) = pack8(x + 8 * j);
-    }
-  }
-  if (HOUT == 0) return;
-  float ss = 0.f;
-#pragma unroll
-  for (int e = 0; e < 32; ++e) ss = fmaf(x[e], x[e], ss);
-  const float rstd = rsqrtf(row_reduce<false>(ss, red[1], warp, w, warps) / (float)a.C + a.norm_eps);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = blk * 128 + j * 32 + l * 8;
-    if (mod && ok) {
-      float sh[8], sc[8];
-      load8(mod + c, sh);
-      load8(mod + a.C + c, sc);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[8 * j + e] = fmaf(x[8 * j + e] * rstd, 1.f + sc[e], sh[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[8 * j + e] *= rstd;
-    }
-  }
-  if (HOUT == 1) {
-    if (ok)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(a.h + base + 32 * j) = pack8(x + 8 * j);
-    return;
-  }
-  constexpr int FMT = HOUT == 3 ? kFp4NV : kFp4MX;
-  constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
-  if (ROT) fwht128_group(x, lane);
-  float am[4];
-  chunk_amax(x, am);
-  const Fp4Row o{a.codes + row * (a.C >> 1), a.scales, row, a.C, katoms};
-  uint32_t q[4], sc;
-  float rs = 1.f;
-  if (FMT == kFp4MX) {
-    quant_mx(x, am, q, sc);
-  } else {
-    const float top = row_reduce<true>(nv_block_amax(am), red[2], warp, w, warps);
-    const int e = nv_row_exponent(top);
-    quant_nv(x, am, e, q, sc);
-    rs = __uint_as_float((uint32_t)(127 + e) << 23);
-  }
-  store_group<FMT>(ok, o, blk, lane, q, sc);
-  if (row < a.rows && w == 0 && lane == 0) a.row_scale[row] = ROT ? rs * kRot : rs;
+  for (int e = 0; e < 8; e += 2)
+    f2_unpack(f2_fma(f2_mul(f2_pack(a[e], a[e + 1]), f2_pack(s, s)), f2_pack(b[e], b[e + 1]), f2_pack(c[e], c[e + 1])),
+              v[e], v[e + 1]);
 }
 
-template <int HOUT, bool ROT>
+// Unnormalised Hadamard transform of 128 channels held eight to a lane by 16
+// lanes.
+__device__ __forceinline__ void fwht128_lanes(float (&h)[8], int lane) {
+#pragma unroll
+  for (int b = 1; b < 8; b <<= 1)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (!(e & b)) {
+        const float u = h[e], w = h[e + b];
+        h[e] = u + w;
+        h[e + b] = u - w;
+      }
+#pragma unroll
+  for (int m = 1; m < 16; m <<= 1) {
+    const float sg = (lane & m) ? -1.f : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = fmaf(sg, h[e], __shfl_xor_sync(0xffffffffu, h[e], m));
+  }
+}
+
+// A thread's eight channels of the key's vectors.
+struct Vectors {
+  float g[8], sh[8], sc[8];  // gate * gain, shift, 1 + scale
+};
+
+// HOUT: 0 no h, 1 bf16, 2 MX, 3 NV. CPT chunks of eight channels per thread
+// (chunk threadIdx.x + i * blockDim.x); the vectors stay in registers for one
+// chunk and are read per row for two.
+template <int HOUT, bool ROT, int CPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, int stages, int katoms) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ float red[2][3][32];
+  __shared__ int keys[kSortRows];
+  __shared__ uint16_t ord[kSortRows];
+  __shared__ int fail[2];
+  const int lane = threadIdx.x & 31;
+  const int nchunk = a.C >> 3;
+  const uint32_t row_bytes = (uint32_t)a.C * 2u;
+  const int64_t per = (a.rows + gridDim.x - 1) / gridDim.x;
+  const int64_t s0 = (int64_t)blockIdx.x * per;
+  const int64_t s1 = s0 + per < a.rows ? s0 + per : a.rows;
+  if (s0 >= s1) return;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+    fail[0] = fail[1] = 0;
+    fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < 2 * 3 * 32; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+  Vectors vec[CPT];
+  int cur = -2;  // key of the vectors held
+  auto load_vectors = [&](int key) {
+    const float* gate = a.table + ((int64_t)key * 6 + a.gate_idx) * a.C;
+    const float* mod = HOUT ? a.norm_table + ((int64_t)key * 6 + a.shift_idx) * a.C : nullptr;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) vec[i].g[e] = vec[i].sh[e] = 0.f, vec[i].sc[e] = 1.f;
+      if (key >= 0 && c < nchunk) {
+        load8(gate + c * 8, vec[i].g);
+        if (HOUT) {
+          load8(mod + c * 8, vec[i].sh);
+          load8(mod + a.C + c * 8, vec[i].sc);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) vec[i].sc[e] += 1.f;
+        }
+        if (a.post_gain) {
+          float pg[8];
+          unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(a.post_gain) + c), pg);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) vec[i].g[e] *= pg[e];
+        }
+      }
+    }
+  };
+  int st = 0, phase = 0, par = 0;  // ring slot and its phase, row parity
+  for (int64_t c0 = s0; c0 < s1; c0 += kSortRows) {
+    const int n = (int)(s1 - c0 < kSortRows ? s1 - c0 : kSortRows);
+    __syncthreads();  // the last group's order is no longer read; the barriers are initialised
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int tg = a.tag[c0 + i], ti = a.tidx[c0 + i];
+      keys[i] = (tg >= 0 && tg < a.n_tags && ti >= 0 && ti < a.n_t) ? tg * a.n_t + ti : -1;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int ki = keys[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const int kj = keys[j];
+        rank += (kj < ki) || (kj == ki && j < i);
+      }
+      ord[rank] = (uint16_t)i;
+    }
+    __syncthreads();
+    // the group's i-th row into a slot
+    auto issue = [&](int i, int slot) {
+      if (i >= n) return;
+      const int64_t at = (c0 + ord[i]) * a.C;
+      uint8_t* dst = ring + (uint32_t)slot * 2 * row_bytes;
+      mbar_expect_tx(&full[slot], 2 * row_bytes);
+      bulk_load(dst, a.x + at, row_bytes, &full[slot]);
+      bulk_load(dst + row_bytes, a.y + at, row_bytes, &full[slot]);
+    };
+    if (threadIdx.x == 0) {
+      fence_proxy_async_smem();  // the slots' last generic reads come before these copies
+      for (int i = 0, slot = st; i < stages; ++i, slot = slot + 1 == stages ? 0 : slot + 1) issue(i, slot);
+    }
+    for (int k = 0; k < n; ++k) {
+      const int idx = ord[k];
+      const int64_t row = c0 + idx;
+      float(&rd)[3][32] = red[par];
+      const int key = keys[idx];
+      if (key != cur) {
+        if (CPT == 1) load_vectors(key);
+        cur = key;
+      }
+      if (!mbar_wait(&full[st], phase, nullptr)) fail[par] = 1;
+      float x[CPT][8], y[CPT][8];
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        uint4 xv = make_uint4(0, 0, 0, 0), yv = xv;
+        if (c < nchunk) {
+          const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)st * 2 * row_bytes);
+          xv = src[c];
+          yv = src[nchunk + c];
+        }
+        unpack_bf16x8(xv, x[i]);
+        unpack_bf16x8(yv, y[i]);
+        if (a.post_norm) ss += squares8(y[i]);
+      }
+      // a barrier: every thread has read the slot, which is refilled, or the
+      // CTA stops because a load never landed
+      const float ssy = cta_reduce<false>(ss, rd[0]);
+      if (fail[par]) {
+        if (threadIdx.x == 0)
+          for (int i = k; i < k + stages && i < n; ++i) {
+            mbar_wait(&full[st], phase, nullptr);
+            if (++st == stages) st = 0, phase ^= 1;
+          }
+        return;
+      }
+      if (threadIdx.x == 0) {
+        fail[par ^ 1] = 0;  // every thread passed the last row's check of that flag
+        fence_proxy_async_smem();
+        issue(k + stages, st);
+      }
+      if (++st == stages) st = 0, phase ^= 1;
+      par ^= 1;
+      float rp = a.branch_scale;
+      if (a.post_norm) rp *= rsqrtf(ssy / (float)a.C + a.post_eps);
+      if (CPT > 1) load_vectors(key);
+      ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (key >= 0)  // (a zero gate times an infinite y would not leave x as it is)
+          scale_fma8(x[i], vec[i].g, rp, y[i], x[i]);
+        if (c < nchunk) reinterpret_cast<uint4*>(a.x_out + row * a.C)[c] = pack8(x[i]);
+        ss += squares8(x[i]);
+      }
+      if (HOUT == 0) continue;
+      const float rstd = rsqrtf(cta_reduce<false>(ss, rd[1]) / (float)a.C + a.norm_eps);
+      float am[CPT], top = 0.f;
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        scale_fma8(x[i], x[i], rstd, vec[i].sc, vec[i].sh);
+        if (HOUT == 1) {
+          if (c < nchunk) reinterpret_cast<uint4*>(a.h + row * a.C)[c] = pack8(x[i]);
+          continue;
+        }
+        if (ROT) fwht128_lanes(x[i], lane);
+        am[i] = fabsf(x[i][0]);
+#pragma unroll
+        for (int e = 1; e < 8; ++e) am[i] = max_nan(am[i], fabsf(x[i][e]));
+        am[i] = max_nan(am[i], __shfl_xor_sync(0xffffffffu, am[i], 1));
+        if (HOUT == 2) am[i] = max_nan(am[i], __shfl_xor_sync(0xffffffffu, am[i], 2));
+        if (HOUT == 3 && finite_bits(am[i])) top = fmaxf(top, am[i]);
+      }
+      if (HOUT == 1) continue;
+      constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
+      int e_row = 0;
+      if (HOUT == 3) e_row = nv_row_exponent(cta_reduce<true>(top, rd[2]));
+      if (threadIdx.x == 0) a.row_scale[row] = pow2_float(e_row) * (ROT ? kRot : 1.f);
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        uint32_t sc;
+        const uint32_t q = HOUT == 2 ? quant8_mx(x[i], am[i], sc) : quant8_nv(x[i], am[i], pow2_float(-e_row), sc);
+        if (c < nchunk) reinterpret_cast<uint32_t*>(a.codes + row * (a.C >> 1))[c] = q;
+        // the four scale bytes of an atom's row, gathered from the lanes of 4
+        // blocks (MX: 16 lanes, four to a block; NV: 8 lanes, two to a block)
+        constexpr int kBlk = HOUT == 2 ? 4 : 2;
+        sc <<= 8 * ((lane / kBlk) & 3);
+        sc |= __shfl_xor_sync(0xffffffffu, sc, kBlk);
+        sc |= __shfl_xor_sync(0xffffffffu, sc, 2 * kBlk);
+        if (c < nchunk && lane % (4 * kBlk) == 0) *fp4_scale_word(a.scales, row, katoms, c / (4 * kBlk)) = sc;
+      }
+    }
+  }
+}
+
+template <int HOUT, bool ROT, int CPT, int MAXT>
 cudaError_t launch_t(const SandwichArgs& a, cudaStream_t s) {
-  const int warps = (a.C + 1023) / 1024;
-  if (warps > kMaxRowWarps) return cudaErrorInvalidValue;
-  const int per_cta = warps >= kSmallCta ? 1 : kSmallCta / warps;
-  const int64_t grid = (a.rows + per_cta - 1) / per_cta;
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  sandwich_kernel<HOUT, ROT>
-      <<<(unsigned)grid, 32 * warps * per_cta, 0, s>>>(a, warps, HOUT >= 2 ? fp4_katoms(HOUT == 3 ? kFp4NV : kFp4MX, a.C) : 0);
+  auto kern = sandwich_kernel<HOUT, ROT, CPT, MAXT>;
+  const int threads = ((a.C / 8 + CPT - 1) / CPT + 31) / 32 * 32;
+  // four rows ahead, up to eight of narrow ones, three of the widest
+  const size_t stage = (size_t)a.C * 4;
+  int stages = (int)((a.C <= 2048 ? 32 * 1024 : 192 * 1024) / stage);
+  stages = stages > (a.C <= 2048 ? kMaxStages : 4) ? (a.C <= 2048 ? kMaxStages : 4) : stages;
+  const size_t smem = stages * stage;
+  cudaError_t e;
+  if (smem > 40 * 1024 &&
+      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    return e;
+  int dev = 0, sms = 0, per_sm = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return e;
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  const int64_t grid = a.rows < (int64_t)sms * per_sm ? a.rows : (int64_t)sms * per_sm;
+  kern<<<(unsigned)grid, threads, smem, s>>>(a, stages, HOUT >= 2 ? fp4_katoms(HOUT == 3 ? kFp4NV : kFp4MX, a.C) : 0);
   return cudaGetLastError();
+}
+
+// Thread bounds by width, so that narrow rows leave registers for the vectors.
+template <int HOUT, bool ROT>
+cudaError_t launch_w(const SandwichArgs& a, cudaStream_t s) {
+  if (a.C <= 2048) return launch_t<HOUT, ROT, 1, 256>(a, s);
+  if (a.C <= 5632) return launch_t<HOUT, ROT, 1, 704>(a, s);
+  if (a.C <= 8192) return launch_t<HOUT, ROT, 1, 1024>(a, s);
+  return launch_t<HOUT, ROT, 2, 1024>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_sandwich(const SandwichArgs& a, cudaStream_t s) {
   if (a.rows <= 0) return cudaSuccess;
-  if (a.norm_table == nullptr) return launch_t<0, false>(a, s);
-  if (a.h) return launch_t<1, false>(a, s);
-  if (a.nv) return a.rotate ? launch_t<3, true>(a, s) : launch_t<3, false>(a, s);
-  return a.rotate ? launch_t<2, true>(a, s) : launch_t<2, false>(a, s);
+  if (a.C % 128 || a.C > 16384) return cudaErrorInvalidValue;
+  if (a.norm_table == nullptr) return launch_w<0, false>(a, s);
+  if (a.h) return launch_w<1, false>(a, s);
+  if (a.nv) return a.rotate ? launch_w<3, true>(a, s) : launch_w<3, false>(a, s);
+  return a.rotate ? launch_w<2, true>(a, s) : launch_w<2, false>(a, s);
 }
 
 }  // namespace h3
