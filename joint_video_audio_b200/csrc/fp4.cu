@@ -3,10 +3,7 @@
 // Layout, formats and the arithmetic of a block: fp4.cuh.
 //
 // Both passes are bound by moving each value in and out once: 2 + 0.5 bytes a
-// value and its block scale. A row is spread over whole warps, four lanes to a
-// block of 128 channels; NV needs the row's largest magnitude before its first
-// code, so a CTA holds its rows in registers across one reduction, and MX runs
-// without any barrier.
+// value and its block scale.
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"
@@ -16,56 +13,99 @@ namespace h3 {
 namespace {
 
 constexpr int kMaxRowWarps = 16;  // 1024 channels each: K <= 16384
-constexpr int kSmallCta = 8;      // warps of a CTA whose rows take one warp each
+constexpr int kMaxStages = 4;
 
-// warps: warps per row; a CTA holds blockDim.x / (32 * warps) rows.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Persistent CTAs of as many warps as a row of 1024 channels each takes, one
+// row at a time (row = blockIdx.x + i * gridDim.x), four lanes to a block of
+// 128 channels. Rows arrive by bulk copies issued `stages` rows ahead. NV needs
+// the row's largest magnitude before its first code: the barrier that hands a
+// slot back for refilling is also that reduction's.
 template <int FMT, bool ROT>
-__global__ void __launch_bounds__(kMaxRowWarps * 32) quantize_fp4_kernel(const __nv_bfloat16* __restrict__ in, int64_t ld,
-                                                                       int64_t rows, int K, int katoms, int warps,
-                                                                       uint8_t* __restrict__ codes,
-                                                                       uint8_t* __restrict__ scales,
-                                                                       float* __restrict__ row_scale) {
-  __shared__ float red[kMaxRowWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_cta = (blockDim.x >> 5) / warps;
-  const int64_t row = (int64_t)blockIdx.x * per_cta + warp / warps;
-  const int w = warp % warps;
-  const int blk = w * 8 + (lane >> 2), l = lane & 3;
-  const bool row_ok = row < rows;
-  float h[32];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = blk * 128 + j * 32 + l * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row_ok && c < K) v = __ldg(reinterpret_cast<const uint4*>(in + row * ld + c));
-    unpack_bf16x8(v, h + 8 * j);
+__global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
+    quantize_fp4_kernel(const __nv_bfloat16* __restrict__ in, int64_t ld, int64_t rows, int K, int katoms, int stages,
+                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, float* __restrict__ row_scale) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ float red[2][kMaxRowWarps];
+  __shared__ int fail[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int blk = threadIdx.x >> 2, l = threadIdx.x & 3;
+  const uint32_t row_bytes = (uint32_t)K * 2u;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+    fail[0] = fail[1] = 0;
+    fence_mbar_init();
   }
-  if (ROT) fwht128_group(h, lane);
-  float am[4];
-  chunk_amax(h, am);
-  const Fp4Row o{codes + row * (K >> 1), scales, row, K, katoms};
-  const bool store = row_ok && blk * 128 < K;
-  uint32_t q[4], sc;
-  constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
-  if (FMT == kFp4MX) {
-    quant_mx(h, am, q, sc);
-    store_group<FMT>(store, o, blk, lane, q, sc);
-    if (row_ok && w == 0 && lane == 0) row_scale[row] = ROT ? kRot : 1.f;
-  } else {
-    float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(nv_block_amax(am))));
-    if (warps > 1) {
-      if (lane == 0) red[warp] = top;
-      __syncthreads();
-      const int first = warp - w;
-      for (int i = 0; i < warps; ++i) top = fmaxf(top, red[first + i]);
+  __syncthreads();
+  auto issue = [&](int64_t row, int slot) {
+    if (row >= rows) return;
+    mbar_expect_tx(&full[slot], row_bytes);
+    bulk_load(ring + (uint32_t)slot * row_bytes, in + row * ld, row_bytes, &full[slot]);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < stages; ++i) issue(blockIdx.x + (int64_t)i * gridDim.x, i);
+  int st = 0, phase = 0, par = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
+    if (!mbar_wait(&full[st], phase, nullptr)) fail[par] = 1;
+    // the lane's chunks; odd groups read theirs in the order 1, 0, 3, 2, so
+    // that the two groups of a shared-memory phase take different banks
+    const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)st * row_bytes) + blk * 16 + l;
+    const bool odd = blk & 1;
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int jj = j ^ (odd ? 1 : 0);
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (blk * 128 + jj * 32 + l * 8 < K) v[j] = src[jj * 4];
     }
-    const int e = nv_row_exponent(top);
-    quant_nv(h, am, e, q, sc);
-    store_group<FMT>(store, o, blk, lane, q, sc);
-    if (row_ok && w == 0 && lane == 0) {
-      const float rs = __uint_as_float((uint32_t)(127 + e) << 23);
-      row_scale[row] = ROT ? rs * kRot : rs;
+    float h[32];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 p = v[j], q = v[j ^ 1];
+      unpack_bf16x8(odd ? q : p, h + 8 * j);
     }
+    float am[4], top = 0.f;
+    if (ROT) fwht128_group(h, lane);
+    chunk_amax(h, am);
+    if (FMT == kFp4NV) {
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(nv_block_amax(am))));
+      if (lane == 0) red[par][warp] = top;
+    }
+    __syncthreads();  // every thread has read the slot
+    if (fail[par]) {  // a load never landed: those in flight must before the CTA's shared memory goes
+      if (threadIdx.x == 0)
+        for (int i = 0; i < stages && row + (int64_t)i * gridDim.x < rows; ++i) {
+          mbar_wait(&full[st], phase, nullptr);
+          if (++st == stages) st = 0, phase ^= 1;
+        }
+      return;
+    }
+    if (threadIdx.x == 0) {
+      fail[par ^ 1] = 0;  // every thread passed the last row's check of that flag
+      fence_proxy_async_smem();
+      issue(row + (int64_t)stages * gridDim.x, st);
+    }
+    if (++st == stages) st = 0, phase ^= 1;
+    const Fp4Row o{codes + row * (K >> 1), scales, row, K, katoms};
+    uint32_t q[4], sc;
+    float rs = 1.f;
+    if (FMT == kFp4MX) {
+      quant_mx(h, am, q, sc);
+    } else {
+      for (int i = 0; i < warps; ++i) top = fmaxf(top, red[par][i]);
+      const int e = nv_row_exponent(top);
+      quant_nv(h, am, e, q, sc);
+      rs = pow2_float(e);
+    }
+    store_group<FMT>(blk * 128 < K, o, blk, lane, q, sc);
+    constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
+    if (threadIdx.x == 0) row_scale[row] = ROT ? rs * kRot : rs;
   }
 }
 
@@ -125,13 +165,23 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
 
 template <int FMT, bool ROT>
 cudaError_t launch_quant_t(const Fp4QuantArgs& a, cudaStream_t s) {
-  const int warps = (a.K + 1023) / 1024;
-  if (warps > kMaxRowWarps) return cudaErrorInvalidValue;
-  const int per_cta = warps >= kSmallCta ? 1 : kSmallCta / warps;
-  const int64_t grid = (a.rows + per_cta - 1) / per_cta;
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  quantize_fp4_kernel<FMT, ROT><<<(unsigned)grid, 32 * warps * per_cta, 0, s>>>(
-      a.in, a.ld, a.rows, a.K, fp4_katoms(FMT, a.K), warps, a.codes, a.scales, a.row_scale);
+  auto kern = quantize_fp4_kernel<FMT, ROT>;
+  const int threads = 32 * ((a.K + 1023) / 1024);
+  if (threads > 32 * kMaxRowWarps) return cudaErrorInvalidValue;
+  const int stages = a.K <= 2048 ? kMaxStages : 3;
+  const size_t smem = (size_t)stages * a.K * 2;
+  cudaError_t e;
+  if (smem > 40 * 1024 &&
+      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    return e;
+  int dev = 0, sms = 0, per_sm = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return e;
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  const int64_t grid = a.rows < (int64_t)sms * per_sm ? a.rows : (int64_t)sms * per_sm;
+  kern<<<(unsigned)grid, threads, smem, s>>>(a.in, a.ld, a.rows, a.K, fp4_katoms(FMT, a.K), stages, a.codes, a.scales,
+                                             a.row_scale);
   return cudaGetLastError();
 }
 

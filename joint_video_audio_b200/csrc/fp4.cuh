@@ -210,17 +210,28 @@ __device__ __forceinline__ int nv_row_exponent(float amax) {
   const int e = (int)(bits >> 23) - 127 - 11 + ((bits & 0x7fffffu) > 0x280000u ? 1 : 0);  // 2688 = 1.3125 * 2^11
   return e < -126 ? -126 : e;
 }
+// a / b correctly rounded up to the last place's tie, from an approximate r of
+// 1 / b: one Newton step with the exact remainder. Where the quotient is itself
+// a float (as a value halfway between two codes is), it is found exactly.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Eight values of an NV block with largest magnitude `amax`, in a row of scale
 // 1 / inv_row -> codes and the block's scale byte, amax / 6 in e4m3. The
-// quotient u / s is rounded correctly (one Newton step with the exact
-// remainder), so a value halfway between two codes is seen as such. It is
-// taken as -u / s, whose steps keep the sign of a zero, and the codes' signs
-// are flipped at the end.
+// quotient u / s is taken as in quotient(), negated: -u / s keeps the sign of a
+// zero, and the codes' signs are flipped at the end.
 __device__ __forceinline__ uint32_t quant8_nv(float* h, float amax, float inv_row, uint32_t& scale) {
   const bool ok = finite_bits(amax);
-  scale = ok ? e4m3_code(__fdiv_rn(amax * inv_row, 6.f)) : 0x7fu;
+  scale = ok ? e4m3_code(quotient(amax * inv_row, 6.f, 1.f / 6.f)) : 0x7fu;
   const float s = ok ? e4m3_value(scale) : 0.f;
-  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  const float r = s > 0.f ? rcp_approx(s) : 0.f;
   const uint64_t inv2 = f2_pack(inv_row, inv_row), nr2 = f2_pack(-r, -r), s2 = f2_pack(s, s);
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
