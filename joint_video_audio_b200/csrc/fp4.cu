@@ -26,6 +26,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // 128 channels. Rows arrive by bulk copies issued `stages` rows ahead. NV needs
 // the row's largest magnitude before its first code: the barrier that hands a
 // slot back for refilling is also that reduction's.
+//
+// A lane works on four chunks, w = 0..3: unrotated chunk 4 w + l of its group's
+// block (l = lane % 4; loads of a chunk take 64 contiguous bytes a group, an MX
+// block is chunk w of the four lanes, an NV block that of a lane pair), rotated
+// as fwht128_warp leaves them.
 template <int FMT, bool ROT>
 __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
     quantize_fp4_kernel(const __nv_bfloat16* __restrict__ in, int64_t ld, int64_t rows, int K, int katoms, int stages,
@@ -53,28 +58,31 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
   int st = 0, phase = 0, par = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
     if (!mbar_wait(&full[st], phase, nullptr)) fail[par] = 1;
-    // the lane's chunks; odd groups read theirs in the order 1, 0, 3, 2, so
-    // that the two groups of a shared-memory phase take different banks
-    const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)st * row_bytes) + blk * 16 + l;
-    const bool odd = blk & 1;
+    // the lane's chunks; odd blocks take theirs in swapped pairs, so that the
+    // two groups of a shared-memory phase take different banks
+    const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)st * row_bytes) + blk * 16;
+    const int odd = blk & 1;
     uint4 v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int jj = j ^ (odd ? 1 : 0);
-      v[j] = make_uint4(0, 0, 0, 0);
-      if (blk * 128 + jj * 32 + l * 8 < K) v[j] = src[jj * 4];
+    for (int w = 0; w < 4; ++w) {
+      const int c = ROT ? (w >> 1) * 8 + 2 * l + ((w & 1) ^ odd) : 4 * (w ^ odd) + l;
+      v[w] = make_uint4(0, 0, 0, 0);
+      if (blk * 128 + c * 8 < K) v[w] = src[c];
     }
-    float h[32];
+    float h[32], am[4], top = 0.f;
+    if (ROT) fwht128_warp(v, odd, lane, h);
+    // largest magnitudes of the chunks' blocks; the lanes of a block differ in
+    // the lowest lane bits (rotated: in those above the two lowest)
+    constexpr int kLane = ROT ? 4 : 1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 p = v[j], q = v[j ^ 1];
-      unpack_bf16x8(odd ? q : p, h + 8 * j);
+    for (int w = 0; w < 4; ++w) {
+      am[w] = ROT ? amax8(h + 8 * w) : amax8(v[w]);
+      am[w] = max_nan(am[w], __shfl_xor_sync(0xffffffffu, am[w], kLane));
+      if (FMT == kFp4MX) am[w] = max_nan(am[w], __shfl_xor_sync(0xffffffffu, am[w], 2 * kLane));
+      if (FMT == kFp4NV && finite_bits(am[w])) top = fmaxf(top, am[w]);
     }
-    float am[4], top = 0.f;
-    if (ROT) fwht128_group(h, lane);
-    chunk_amax(h, am);
     if (FMT == kFp4NV) {
-      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(nv_block_amax(am))));
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
       if (lane == 0) red[par][warp] = top;
     }
     __syncthreads();  // every thread has read the slot
@@ -92,20 +100,64 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
       issue(row + (int64_t)stages * gridDim.x, st);
     }
     if (++st == stages) st = 0, phase ^= 1;
-    const Fp4Row o{codes + row * (K >> 1), scales, row, K, katoms};
-    uint32_t q[4], sc;
-    float rs = 1.f;
-    if (FMT == kFp4MX) {
-      quant_mx(h, am, q, sc);
-    } else {
+    int e_row = 0;
+    if (FMT == kFp4NV) {
       for (int i = 0; i < warps; ++i) top = fmaxf(top, red[par][i]);
-      const int e = nv_row_exponent(top);
-      quant_nv(h, am, e, q, sc);
-      rs = pow2_float(e);
+      e_row = nv_row_exponent(top);
     }
-    store_group<FMT>(blk * 128 < K, o, blk, lane, q, sc);
     constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
-    if (threadIdx.x == 0) row_scale[row] = ROT ? rs * kRot : rs;
+    if (threadIdx.x == 0) row_scale[row] = pow2_float(e_row) * (ROT ? kRot : 1.f);
+    uint32_t q[4], sc[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float u[8];
+      if (!ROT) unpack_bf16x8(v[w], u);
+      float* x = ROT ? h + 8 * w : u;
+      q[w] = FMT == kFp4MX ? quant8_mx(x, am[w], sc[w]) : quant8_nv(x, am[w], pow2_float(-e_row), sc[w]);
+    }
+    uint8_t* crow = codes + row * (K >> 1);
+    if (ROT) {
+      // K is a multiple of 128: blocks are whole
+      const int g = lane >> 2;
+      const uint4 c = group_transpose<4>(q, lane);  // four chunks from 4 (g / 4) + 8 (g & 1) of block 2 l + (g / 2 & 1)
+      const int b = warp * 8 + 2 * l;
+      const int bs = b + ((g >> 1) & 1);
+      if (bs * 128 < K) *reinterpret_cast<uint4*>(crow + bs * 64 + (g >> 2) * 16 + (g & 1) * 32) = c;
+      // scale bytes of block b, then b + 1
+      if (FMT == kFp4MX) {
+        uint32_t s0 = sc[0] << (8 * (g >> 2)) | sc[1] << (8 * (g >> 2) + 16);
+        uint32_t s1 = sc[2] << (8 * (g >> 2)) | sc[3] << (8 * (g >> 2) + 16);
+        s0 |= __shfl_xor_sync(0xffffffffu, s0, 16);
+        s1 |= __shfl_xor_sync(0xffffffffu, s1, 16);
+        if (g < 2 && (b + g) * 128 < K) *fp4_scale_word(scales, row, katoms, b + g) = g ? s1 : s0;
+      } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          sc[w] <<= 8 * (g >> 1);
+          sc[w] |= __shfl_xor_sync(0xffffffffu, sc[w], 8);
+          sc[w] |= __shfl_xor_sync(0xffffffffu, sc[w], 16);
+        }
+        // lanes g = 0..3 store the words of atoms 2 b .. 2 b + 3
+        const uint32_t word = g == 0 ? sc[0] : g == 1 ? sc[1] : g == 2 ? sc[2] : sc[3];
+        if (g < 4 && (b + (g >> 1)) * 128 < K) *fp4_scale_word(scales, row, katoms, 2 * b + g) = word;
+      }
+    } else {
+      const uint32_t qs[4] = {odd ? q[1] : q[0], odd ? q[0] : q[1], odd ? q[3] : q[2], odd ? q[2] : q[3]};
+      const uint4 c = group_transpose(qs, lane);
+      const bool ok = blk * 128 < K;
+      if (ok && blk * 128 + l * 32 < K) *reinterpret_cast<uint4*>(crow + blk * 64 + l * 16) = c;
+      uint32_t s = sc[0] | sc[1] << 8 | sc[2] << 16 | sc[3] << 24;
+      s = __byte_perm(s, 0, odd ? 0x2301 : 0x3210);
+      if (FMT == kFp4MX) {
+        if (ok && l == 0) *fp4_scale_word(scales, row, katoms, blk) = s;
+      } else {
+        // lane 0 holds blocks 0, 2, 4, 6 of the 128 channels, lane 2 blocks 1, 3, 5, 7
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, s, 2);
+        if (ok && l == 0) *fp4_scale_word(scales, row, katoms, 2 * blk) = __byte_perm(s, other, 0x5140);
+        if (ok && l == 2 && 2 * blk + 1 < katoms)
+          *fp4_scale_word(scales, row, katoms, 2 * blk + 1) = __byte_perm(other, s, 0x7362);
+      }
+    }
   }
 }
 

@@ -1,5 +1,4 @@
-// Microscaled 4-bit floats: layout, and the quantisation of a 128-channel
-// block held by four lanes.
+// Microscaled 4-bit floats: layout, and the quantisation of a block.
 //
 // A value is an e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign) times its
 // block's scale times its row's scale. Two formats:
@@ -10,11 +9,8 @@
 // core takes them: row r, block b at byte (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4
 // of atom (r / 128) * katoms + b / 4.
 //
-// A thread group of four lanes holds a block of 128 channels: lane l has the
-// eight-channel chunks l, l + 4, l + 8, l + 12, so that global loads of a chunk
-// take 64 contiguous bytes per group, an MX block is one chunk of each of the
-// four lanes, an NV block one chunk of a lane pair, and five of the seven
-// stages of the 128-point Hadamard transform stay inside a thread.
+// Rows are worked on in chunks of eight channels (16 bytes of bf16, one word of
+// codes); an MX block is four chunks, an NV block two.
 #pragma once
 #include <cstdint>
 
@@ -90,74 +86,99 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
   return __uint_as_float(code == 0 ? 0x00400000u : code == 255 ? 0x7fffffffu : code << 23);
 }
 
-// Unnormalised 128-point Walsh-Hadamard transform of a group's block,
-// h[8 j + e] = channel 32 j + 8 l + e of lane l.
-__device__ __forceinline__ void fwht128_group(float (&h)[32], int lane) {
+// Unnormalised 128-point Walsh-Hadamard transforms of the eight blocks a warp
+// holds, bf16 in: H128 = H16 x H8 (Kronecker) with channel = 8 i + e. The
+// 16-point part, across chunks, is a product with the +-1 matrix H16 on the
+// tensor cores (m16n8k16; n = block, one product for each e), exact up to the
+// fp32 sum; the 8-point part then lies inside a lane. Against butterflies with
+// two lane exchanges a value it takes 72 instructions a lane instead of 224.
+//
+// In: lane (b = lane / 4, t = lane % 4) holds chunks 2 t, 2 t + 1, 2 t + 8 and
+// 2 t + 9 of block b, the pairs in the order of `swapped` blocks reversed.
+// Out: lane (g = lane / 4, t): h[0..7] chunk g of block 2 t, h[8..] chunk g + 8
+// of block 2 t, h[16..] chunk g of block 2 t + 1, h[24..] chunk g + 8 of it.
+__device__ __forceinline__ void fwht128_warp(const uint4 (&v)[4], bool swapped, int lane, float (&h)[32]) {
+  const int g = lane >> 2, t = lane & 3;
+  auto pm1 = [](int r, int c) { return (uint32_t)((__popc(r & c) & 1) ? 0xBF80u : 0x3F80u); };
+  auto frag = [&](int r, int c) { return pm1(r, c) | (pm1(r, c + 1) << 16); };
+  const uint32_t a0 = frag(g, 2 * t), a1 = frag(g + 8, 2 * t), a2 = frag(g, 2 * t + 8), a3 = frag(g + 8, 2 * t + 8);
+  const uint32_t lo = swapped ? 0x1054u : 0x5410u, hi = swapped ? 0x3276u : 0x7632u;
+  const uint32_t w[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w},
+                            {v[1].x, v[1].y, v[1].z, v[1].w},
+                            {v[2].x, v[2].y, v[2].z, v[2].w},
+                            {v[3].x, v[3].y, v[3].z, v[3].w}};
+  float d[8][4];
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    const float u = h[e], w = h[e + 1];
-    h[e] = u + w;
-    h[e + 1] = u - w;
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b0 = __byte_perm(w[0][e >> 1], w[1][e >> 1], (e & 1) ? hi : lo);
+    const uint32_t b1 = __byte_perm(w[2][e >> 1], w[3][e >> 1], (e & 1) ? hi : lo);
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[e][0]), "=f"(d[e][1]), "=f"(d[e][2]), "=f"(d[e][3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
   }
+  // 8-point transforms over e of the four (chunk, block) results
 #pragma unroll
-  for (int b = 2; b < 32; b <<= 1) {  // channel bits 1, 2 (in a chunk) and 5, 6 (across the lane's chunks)
+  for (int q = 0; q < 4; ++q) {
+    const int c = (q & 1) * 2 + (q >> 1);  // h order: chunk g, g + 8 of block 2 t, then of block 2 t + 1
+    uint64_t p[4];
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      if (!(e & b)) {
-        const uint64_t u = f2_pack(h[e], h[e + 1]), w = f2_pack(h[e + b], h[e + b + 1]);
-        f2_unpack(f2_add(u, w), h[e], h[e + 1]);
-        f2_unpack(f2_fma(w, f2_pack(-1.f, -1.f), u), h[e + b], h[e + b + 1]);
-      }
+    for (int e = 0; e < 8; e += 2) {  // bit 0
+      const float u = d[e][c], x = d[e + 1][c];
+      p[e >> 1] = f2_pack(u + x, u - x);
     }
-  }
+    const uint64_t m1 = f2_pack(-1.f, -1.f);
 #pragma unroll
-  for (int m = 1; m <= 2; m <<= 1) {  // channel bits 3, 4: the lower lane takes h + other, the upper other - h
-    const float sg = (lane & m) ? -1.f : 1.f;
-    const uint64_t sg2 = f2_pack(sg, sg);
+    for (int bit = 1; bit <= 2; bit <<= 1)
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const float o0 = __shfl_xor_sync(0xffffffffu, h[e], m), o1 = __shfl_xor_sync(0xffffffffu, h[e + 1], m);
-      f2_unpack(f2_fma(sg2, f2_pack(h[e], h[e + 1]), f2_pack(o0, o1)), h[e], h[e + 1]);
-    }
+      for (int e = 0; e < 4; ++e)
+        if (!(e & bit)) {
+          const uint64_t u = p[e], x = p[e + bit];
+          p[e] = f2_add(u, x);
+          p[e + bit] = f2_fma(x, m1, u);
+        }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f2_unpack(p[e], h[8 * q + 2 * e], h[8 * q + 2 * e + 1]);
   }
 }
 
-// Lane l's words of four chunk columns (chunk 4 j + l in w[j]) to the words of
-// its own row quarter (chunk 4 l + j): a 4 x 4 transpose inside the group.
-// It is its own inverse.
+// A 4 x 4 transpose of words among the four lanes that differ in lane bits
+// LANE and 2 LANE: lane q of them gets word q of each, in lane order.
+template <int LANE = 1>
 __device__ __forceinline__ uint4 group_transpose(const uint32_t (&w)[4], int lane) {
-  const bool o1 = lane & 1, o2 = lane & 2;
+  const bool o1 = lane & LANE, o2 = lane & (2 * LANE);
   uint32_t a0 = w[0], a1 = w[1], a2 = w[2], a3 = w[3];
-  uint32_t s0 = __shfl_xor_sync(0xffffffffu, o1 ? a0 : a1, 1);
-  uint32_t s1 = __shfl_xor_sync(0xffffffffu, o1 ? a2 : a3, 1);
-  if (o1) {
-    a0 = s0;
-    a2 = s1;
-  } else {
-    a1 = s0;
-    a3 = s1;
-  }
-  s0 = __shfl_xor_sync(0xffffffffu, o2 ? a0 : a2, 2);
-  s1 = __shfl_xor_sync(0xffffffffu, o2 ? a1 : a3, 2);
-  if (o2) {
-    a0 = s0;
-    a1 = s1;
-  } else {
-    a2 = s0;
-    a3 = s1;
-  }
+  uint32_t s0 = __shfl_xor_sync(0xffffffffu, o1 ? a0 : a1, LANE);
+  uint32_t s1 = __shfl_xor_sync(0xffffffffu, o1 ? a2 : a3, LANE);
+  a0 = o1 ? s0 : a0;
+  a2 = o1 ? s1 : a2;
+  a1 = o1 ? a1 : s0;
+  a3 = o1 ? a3 : s1;
+  s0 = __shfl_xor_sync(0xffffffffu, o2 ? a0 : a2, 2 * LANE);
+  s1 = __shfl_xor_sync(0xffffffffu, o2 ? a1 : a3, 2 * LANE);
+  a0 = o2 ? s0 : a0;
+  a1 = o2 ? s1 : a1;
+  a2 = o2 ? a2 : s0;
+  a3 = o2 ? a3 : s1;
   return make_uint4(a0, a1, a2, a3);
 }
 
-// Largest magnitude of each of a lane's four chunks.
-__device__ __forceinline__ void chunk_amax(const float (&h)[32], float (&am)[4]) {
+// Largest magnitude of eight values (NaN if one is).
+__device__ __forceinline__ float amax8(const float* h) {
+  float a = fabsf(h[0]);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float a = fabsf(h[8 * j]);
-#pragma unroll
-    for (int e = 1; e < 8; ++e) a = max_nan(a, fabsf(h[8 * j + e]));
-    am[j] = a;
-  }
+  for (int e = 1; e < 8; ++e) a = max_nan(a, fabsf(h[e]));
+  return a;
+}
+// The same of eight bf16 values.
+__device__ __forceinline__ float amax8(const uint4& v) {
+  auto mx = [](uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  };
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t r = mx(mx(v.x & m, v.y & m), mx(v.z & m, v.w & m));
+  return max_nan(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
 }
 
 // Eight values of an MX block with largest magnitude `amax` -> codes and the
@@ -176,31 +197,6 @@ __device__ __forceinline__ uint32_t quant8_mx(float* h, float amax, uint32_t& sc
 #pragma unroll
   for (int e = 0; e < 8; e += 2) f2_unpack(f2_mul(f2_pack(h[e], h[e + 1]), inv2), h[e], h[e + 1]);
   return e2m1x8(h);
-}
-// MX: am[j] of the lane's chunks -> the group's codes and its four scale bytes
-// (the same word in every lane).
-__device__ __forceinline__ void quant_mx(float (&h)[32], float (&am)[4], uint32_t (&codes)[4], uint32_t& scale_word) {
-  scale_word = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    am[j] = max_nan(am[j], __shfl_xor_sync(0xffffffffu, am[j], 1));
-    am[j] = max_nan(am[j], __shfl_xor_sync(0xffffffffu, am[j], 2));
-    uint32_t sc;
-    codes[j] = quant8_mx(h + 8 * j, am[j], sc);
-    scale_word |= sc << (8 * j);
-  }
-}
-
-// NV, first half: am[j] becomes the largest magnitude of the lane pair's
-// block; returns the largest finite one (0 if none).
-__device__ __forceinline__ float nv_block_amax(float (&am)[4]) {
-  float top = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    am[j] = max_nan(am[j], __shfl_xor_sync(0xffffffffu, am[j], 1));
-    if (finite_bits(am[j])) top = fmaxf(top, am[j]);
-  }
-  return top;
 }
 // Exponent E of a row's scale 2^E: the smallest with amax <= 448 * 6 * 2^E, so
 // that the largest block scale lies in the upper binade of e4m3. 0 for a zero row.
@@ -242,47 +238,6 @@ __device__ __forceinline__ uint32_t quant8_nv(float* h, float amax, float inv_ro
   return e2m1x8(h) ^ 0x88888888u;
 }
 __device__ __forceinline__ float pow2_float(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-// NV, second half: codes and the lane's four scale bytes, one per chunk (byte
-// j: block 2 j + l / 2 of the 128 channels).
-__device__ __forceinline__ void quant_nv(float (&h)[32], const float (&am)[4], int row_exp, uint32_t (&codes)[4],
-                                         uint32_t& scale_bytes) {
-  scale_bytes = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t sc;
-    codes[j] = quant8_nv(h + 8 * j, am[j], pow2_float(-row_exp), sc);
-    scale_bytes |= sc << (8 * j);
-  }
-}
-
-// Where a row's 4-bit form goes.
-struct Fp4Row {
-  uint8_t* codes;   // the row's first byte
-  uint8_t* scales;  // the whole scale tensor
-  int64_t row;
-  int K, katoms;
-};
-
-// Stores a group's block `blk` (128 channels from 128 blk) where `ok` (the same
-// for the four lanes). Every lane of the warp calls it. Chunks past K hold
-// zeros; whole quarters past K are not stored.
-template <int FMT>
-__device__ __forceinline__ void store_group(bool ok, const Fp4Row& o, int blk, int lane, const uint32_t (&codes)[4],
-                                            uint32_t scale) {
-  const int l = lane & 3;
-  const uint4 c = group_transpose(codes, lane);
-  if (ok && blk * 128 + l * 32 < o.K) *reinterpret_cast<uint4*>(o.codes + blk * 64 + l * 16) = c;
-  if (FMT == kFp4MX) {
-    if (ok && l == 0) *fp4_scale_word(o.scales, o.row, o.katoms, blk) = scale;
-  } else {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, scale, 2);
-    // lane 0 holds blocks 0, 2, 4, 6 of the 128 channels, lane 2 blocks 1, 3, 5, 7
-    if (ok && l == 0) *fp4_scale_word(o.scales, o.row, o.katoms, 2 * blk) = __byte_perm(scale, other, 0x5140);
-    if (ok && l == 2 && 2 * blk + 1 < o.katoms)
-      *fp4_scale_word(o.scales, o.row, o.katoms, 2 * blk + 1) = __byte_perm(other, scale, 0x7362);
-  }
-}
-
 __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
