@@ -21,16 +21,35 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// A 4 x 4 transpose of words among four neighbouring lanes: lane q of them gets
+// word q of each, in lane order.
+__device__ __forceinline__ uint4 group_transpose(const uint32_t (&w)[4], int lane) {
+  const bool o1 = lane & 1, o2 = lane & (2);
+  uint32_t a0 = w[0], a1 = w[1], a2 = w[2], a3 = w[3];
+  uint32_t s0 = __shfl_xor_sync(0xffffffffu, o1 ? a0 : a1, 1);
+  uint32_t s1 = __shfl_xor_sync(0xffffffffu, o1 ? a2 : a3, 1);
+  a0 = o1 ? s0 : a0;
+  a2 = o1 ? s1 : a2;
+  a1 = o1 ? a1 : s0;
+  a3 = o1 ? a3 : s1;
+  s0 = __shfl_xor_sync(0xffffffffu, o2 ? a0 : a2, 2);
+  s1 = __shfl_xor_sync(0xffffffffu, o2 ? a1 : a3, 2);
+  a0 = o2 ? s0 : a0;
+  a1 = o2 ? s1 : a1;
+  a2 = o2 ? a2 : s0;
+  a3 = o2 ? a3 : s1;
+  return make_uint4(a0, a1, a2, a3);
+}
+
 // Persistent CTAs of as many warps as a row of 1024 channels each takes, one
 // row at a time (row = blockIdx.x + i * gridDim.x), four lanes to a block of
 // 128 channels. Rows arrive by bulk copies issued `stages` rows ahead. NV needs
 // the row's largest magnitude before its first code: the barrier that hands a
 // slot back for refilling is also that reduction's.
 //
-// A lane works on four chunks, w = 0..3: unrotated chunk 4 w + l of its group's
-// block (l = lane % 4; loads of a chunk take 64 contiguous bytes a group, an MX
-// block is chunk w of the four lanes, an NV block that of a lane pair), rotated
-// as fwht128_warp leaves them.
+// A lane works on 32 channels: unrotated the 32 from 32 threadIdx.x (an MX
+// block, two NV blocks; its 16-byte reads of the row in an order that gives
+// each eight lanes distinct banks), rotated as fwht128_warp leaves them.
 template <int FMT, bool ROT>
 __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
     quantize_fp4_kernel(const __nv_bfloat16* __restrict__ in, int64_t ld, int64_t rows, int K, int katoms, int stages,
@@ -40,7 +59,7 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
   __shared__ float red[2][kMaxRowWarps];
   __shared__ int fail[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int blk = threadIdx.x >> 2, l = threadIdx.x & 3;
+  const int blk = threadIdx.x >> 2, l = threadIdx.x & 3, g = lane >> 2;
   const uint32_t row_bytes = (uint32_t)K * 2u;
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
@@ -58,28 +77,34 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
   int st = 0, phase = 0, par = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
     if (!mbar_wait(&full[st], phase, nullptr)) fail[par] = 1;
-    // the lane's chunks; odd blocks take theirs in swapped pairs, so that the
-    // two groups of a shared-memory phase take different banks
-    const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)st * row_bytes) + blk * 16;
-    const int odd = blk & 1;
+    // the lane's chunks: slot w holds chunk w ^ perm of its 32 channels;
+    // rotated, odd blocks take theirs in swapped pairs
+    const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)st * row_bytes);
+    const int perm = ROT ? blk & 1 : (threadIdx.x >> 1) & 3;
     uint4 v[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const int c = ROT ? (w >> 1) * 8 + 2 * l + ((w & 1) ^ odd) : 4 * (w ^ odd) + l;
+      const int c = ROT ? blk * 16 + (w >> 1) * 8 + 2 * l + ((w & 1) ^ perm) : threadIdx.x * 4 + (w ^ perm);
       v[w] = make_uint4(0, 0, 0, 0);
-      if (blk * 128 + c * 8 < K) v[w] = src[c];
+      if (c * 8 < K) v[w] = src[c];
     }
-    float h[32], am[4], top = 0.f;
-    if (ROT) fwht128_warp(v, odd, lane, h);
-    // largest magnitudes of the chunks' blocks; the lanes of a block differ in
-    // the lowest lane bits (rotated: in those above the two lowest)
-    constexpr int kLane = ROT ? 4 : 1;
+    // the largest magnitudes of its two groups of 16 channels; of the MX block
+    // that each belongs to
+    float h[32], am[2], top = 0.f;
+    if (ROT) fwht128_warp(v, perm, lane, h);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      am[w] = ROT ? amax8(h + 8 * w) : amax8(v[w]);
-      am[w] = max_nan(am[w], __shfl_xor_sync(0xffffffffu, am[w], kLane));
-      if (FMT == kFp4MX) am[w] = max_nan(am[w], __shfl_xor_sync(0xffffffffu, am[w], 2 * kLane));
-      if (FMT == kFp4NV && finite_bits(am[w])) top = fmaxf(top, am[w]);
+    for (int i = 0; i < 2; ++i)
+      am[i] = ROT ? max_nan(amax8(h + 16 * i), amax8(h + 16 * i + 8)) : max_nan(amax8(v[2 * i]), amax8(v[2 * i + 1]));
+    if (FMT == kFp4MX) {
+      if (ROT) {
+        am[0] = max_nan(am[0], __shfl_xor_sync(0xffffffffu, am[0], 4));
+        am[1] = max_nan(am[1], __shfl_xor_sync(0xffffffffu, am[1], 4));
+      } else {
+        am[0] = max_nan(am[0], am[1]);
+      }
+    } else {
+      if (finite_bits(am[0])) top = am[0];
+      if (finite_bits(am[1])) top = fmaxf(top, am[1]);
     }
     if (FMT == kFp4NV) {
       top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
@@ -107,55 +132,57 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
     }
     constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
     if (threadIdx.x == 0) row_scale[row] = pow2_float(e_row) * (ROT ? kRot : 1.f);
-    uint32_t q[4], sc[4];
+    uint32_t q[4], sc[2];
+    const float inv_row = pow2_float(-e_row);
+    float inv = 0.f;
+    NvScale nv{};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
+      if (FMT == kFp4NV && w % 2 == 0) nv = nv_scale(am[w / 2], inv_row, sc[w / 2]);
+      if (FMT == kFp4MX && (w == 0 || (ROT && w == 2))) inv = mx_scale(am[w / 2], sc[w / 2]);
       float u[8];
       if (!ROT) unpack_bf16x8(v[w], u);
       float* x = ROT ? h + 8 * w : u;
-      q[w] = FMT == kFp4MX ? quant8_mx(x, am[w], sc[w]) : quant8_nv(x, am[w], pow2_float(-e_row), sc[w]);
+      q[w] = FMT == kFp4MX ? quant8_mx(x, inv) : quant8_nv(x, inv_row, nv);
     }
     uint8_t* crow = codes + row * (K >> 1);
     if (ROT) {
-      // K is a multiple of 128: blocks are whole
-      const int g = lane >> 2;
-      const uint4 c = group_transpose<4>(q, lane);  // four chunks from 4 (g / 4) + 8 (g & 1) of block 2 l + (g / 2 & 1)
+      // K is a multiple of 128: blocks are whole. 16 channels each of blocks b, b + 1
       const int b = warp * 8 + 2 * l;
-      const int bs = b + ((g >> 1) & 1);
-      if (bs * 128 < K) *reinterpret_cast<uint4*>(crow + bs * 64 + (g >> 2) * 16 + (g & 1) * 32) = c;
-      // scale bytes of block b, then b + 1
-      if (FMT == kFp4MX) {
-        uint32_t s0 = sc[0] << (8 * (g >> 2)) | sc[1] << (8 * (g >> 2) + 16);
-        uint32_t s1 = sc[2] << (8 * (g >> 2)) | sc[3] << (8 * (g >> 2) + 16);
-        s0 |= __shfl_xor_sync(0xffffffffu, s0, 16);
-        s1 |= __shfl_xor_sync(0xffffffffu, s1, 16);
-        if (g < 2 && (b + g) * 128 < K) *fp4_scale_word(scales, row, katoms, b + g) = g ? s1 : s0;
-      } else {
+      if (b * 128 < K) *reinterpret_cast<uint2*>(crow + b * 64 + g * 8) = make_uint2(q[0], q[1]);
+      if (b * 128 + 128 < K) *reinterpret_cast<uint2*>(crow + b * 64 + 64 + g * 8) = make_uint2(q[2], q[3]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          sc[w] <<= 8 * (g >> 1);
-          sc[w] |= __shfl_xor_sync(0xffffffffu, sc[w], 8);
-          sc[w] |= __shfl_xor_sync(0xffffffffu, sc[w], 16);
+      for (int i = 0; i < 2; ++i) {
+        if (FMT == kFp4MX) {  // byte g / 2 of the block's word
+          sc[i] <<= 8 * (g >> 1);
+          sc[i] |= __shfl_xor_sync(0xffffffffu, sc[i], 8);
+          sc[i] |= __shfl_xor_sync(0xffffffffu, sc[i], 16);
+        } else {  // byte g % 4 of the block's word g / 4
+          sc[i] <<= 8 * (g & 3);
+          sc[i] |= __shfl_xor_sync(0xffffffffu, sc[i], 4);
+          sc[i] |= __shfl_xor_sync(0xffffffffu, sc[i], 8);
         }
-        // lanes g = 0..3 store the words of atoms 2 b .. 2 b + 3
-        const uint32_t word = g == 0 ? sc[0] : g == 1 ? sc[1] : g == 2 ? sc[2] : sc[3];
-        if (g < 4 && (b + (g >> 1)) * 128 < K) *fp4_scale_word(scales, row, katoms, 2 * b + g) = word;
       }
+      const int i = g & 1;  // lanes g = 0, 1 store block b's, b + 1's (first) word, for NV g = 4, 5 the second
+      if ((g & 2) == 0 && (FMT == kFp4NV || g < 4) && (b + i) * 128 < K)
+        *fp4_scale_word(scales, row, katoms, FMT == kFp4MX ? b + i : 2 * (b + i) + (g >> 2)) = i ? sc[1] : sc[0];
     } else {
-      const uint32_t qs[4] = {odd ? q[1] : q[0], odd ? q[0] : q[1], odd ? q[3] : q[2], odd ? q[2] : q[3]};
-      const uint4 c = group_transpose(qs, lane);
-      const bool ok = blk * 128 < K;
-      if (ok && blk * 128 + l * 32 < K) *reinterpret_cast<uint4*>(crow + blk * 64 + l * 16) = c;
-      uint32_t s = sc[0] | sc[1] << 8 | sc[2] << 16 | sc[3] << 24;
-      s = __byte_perm(s, 0, odd ? 0x2301 : 0x3210);
+      // the words back in the channels' order
+      const bool s1 = perm & 1, s2 = perm & 2;
+      const uint32_t a0 = s1 ? q[1] : q[0], a1 = s1 ? q[0] : q[1], a2 = s1 ? q[3] : q[2], a3 = s1 ? q[2] : q[3];
+      const bool ok = threadIdx.x * 32 < K;
+      if (ok)
+        *reinterpret_cast<uint4*>(crow + threadIdx.x * 16) =
+            s2 ? make_uint4(a2, a3, a0, a1) : make_uint4(a0, a1, a2, a3);
       if (FMT == kFp4MX) {
-        if (ok && l == 0) *fp4_scale_word(scales, row, katoms, blk) = s;
+        uint32_t s = (ok ? sc[0] : 1u) << (8 * l);  // (past K: the smallest scale)
+        s |= __shfl_xor_sync(0xffffffffu, s, 1);
+        s |= __shfl_xor_sync(0xffffffffu, s, 2);
+        if (l == 0 && blk * 128 < K) *fp4_scale_word(scales, row, katoms, blk) = s;
       } else {
-        // lane 0 holds blocks 0, 2, 4, 6 of the 128 channels, lane 2 blocks 1, 3, 5, 7
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, s, 2);
-        if (ok && l == 0) *fp4_scale_word(scales, row, katoms, 2 * blk) = __byte_perm(s, other, 0x5140);
-        if (ok && l == 2 && 2 * blk + 1 < katoms)
-          *fp4_scale_word(scales, row, katoms, 2 * blk + 1) = __byte_perm(other, s, 0x7362);
+        uint32_t s = (s2 ? sc[1] | sc[0] << 8 : sc[0] | sc[1] << 8) << (16 * (l & 1));
+        s |= __shfl_xor_sync(0xffffffffu, s, 1);
+        if ((l & 1) == 0 && ok) *fp4_scale_word(scales, row, katoms, 2 * blk + (l >> 1)) = s;
       }
     }
   }

@@ -95,13 +95,15 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
 //
 // In: lane (b = lane / 4, t = lane % 4) holds chunks 2 t, 2 t + 1, 2 t + 8 and
 // 2 t + 9 of block b, the pairs in the order of `swapped` blocks reversed.
-// Out: lane (g = lane / 4, t): h[0..7] chunk g of block 2 t, h[8..] chunk g + 8
-// of block 2 t, h[16..] chunk g of block 2 t + 1, h[24..] chunk g + 8 of it.
+// Out: lane (g = lane / 4, t): h[0..15] chunks 2 g, 2 g + 1 of block 2 t (an NV
+// block), h[16..31] the same chunks of block 2 t + 1: H16's rows are taken in
+// the order 0, 2, .. 14, 1, 3, .. 15.
 __device__ __forceinline__ void fwht128_warp(const uint4 (&v)[4], bool swapped, int lane, float (&h)[32]) {
   const int g = lane >> 2, t = lane & 3;
   auto pm1 = [](int r, int c) { return (uint32_t)((__popc(r & c) & 1) ? 0xBF80u : 0x3F80u); };
   auto frag = [&](int r, int c) { return pm1(r, c) | (pm1(r, c + 1) << 16); };
-  const uint32_t a0 = frag(g, 2 * t), a1 = frag(g + 8, 2 * t), a2 = frag(g, 2 * t + 8), a3 = frag(g + 8, 2 * t + 8);
+  const uint32_t a0 = frag(2 * g, 2 * t), a1 = frag(2 * g + 1, 2 * t);
+  const uint32_t a2 = frag(2 * g, 2 * t + 8), a3 = frag(2 * g + 1, 2 * t + 8);
   const uint32_t lo = swapped ? 0x1054u : 0x5410u, hi = swapped ? 0x3276u : 0x7632u;
   const uint32_t w[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w},
                             {v[1].x, v[1].y, v[1].z, v[1].w},
@@ -119,7 +121,7 @@ __device__ __forceinline__ void fwht128_warp(const uint4 (&v)[4], bool swapped, 
   // 8-point transforms over e of the four (chunk, block) results
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int c = (q & 1) * 2 + (q >> 1);  // h order: chunk g, g + 8 of block 2 t, then of block 2 t + 1
+    const int c = (q & 1) * 2 + (q >> 1);  // h order: chunks 2 g, 2 g + 1 of block 2 t, then of block 2 t + 1
     uint64_t p[4];
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {  // bit 0
@@ -141,27 +143,6 @@ __device__ __forceinline__ void fwht128_warp(const uint4 (&v)[4], bool swapped, 
   }
 }
 
-// A 4 x 4 transpose of words among the four lanes that differ in lane bits
-// LANE and 2 LANE: lane q of them gets word q of each, in lane order.
-template <int LANE = 1>
-__device__ __forceinline__ uint4 group_transpose(const uint32_t (&w)[4], int lane) {
-  const bool o1 = lane & LANE, o2 = lane & (2 * LANE);
-  uint32_t a0 = w[0], a1 = w[1], a2 = w[2], a3 = w[3];
-  uint32_t s0 = __shfl_xor_sync(0xffffffffu, o1 ? a0 : a1, LANE);
-  uint32_t s1 = __shfl_xor_sync(0xffffffffu, o1 ? a2 : a3, LANE);
-  a0 = o1 ? s0 : a0;
-  a2 = o1 ? s1 : a2;
-  a1 = o1 ? a1 : s0;
-  a3 = o1 ? a3 : s1;
-  s0 = __shfl_xor_sync(0xffffffffu, o2 ? a0 : a2, 2 * LANE);
-  s1 = __shfl_xor_sync(0xffffffffu, o2 ? a1 : a3, 2 * LANE);
-  a0 = o2 ? s0 : a0;
-  a1 = o2 ? s1 : a1;
-  a2 = o2 ? a2 : s0;
-  a3 = o2 ? a3 : s1;
-  return make_uint4(a0, a1, a2, a3);
-}
-
 // Largest magnitude of eight values (NaN if one is).
 __device__ __forceinline__ float amax8(const float* h) {
   float a = fabsf(h[0]);
@@ -181,23 +162,26 @@ __device__ __forceinline__ float amax8(const uint4& v) {
   return max_nan(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
 }
 
-// Eight values of an MX block with largest magnitude `amax` -> codes and the
-// block's scale byte. The scale is the smallest 2^e with amax <= 7 * 2^e: an
-// amax in (6, 7] takes the code 6 under 2^e and under 2^(e+1) alike, so the
-// smaller scale is never the worse one. Multiplying by 2^-e is exact, hence so
-// are the codes. A block with a non-finite value gets the NaN scale.
-__device__ __forceinline__ uint32_t quant8_mx(float* h, float amax, uint32_t& scale) {
+// MX: scale byte of a block with largest magnitude `amax`, and the factor 2^-e
+// of its values. The scale is the smallest 2^e with amax <= 7 * 2^e: an amax in
+// (6, 7] takes the code 6 under 2^e and under 2^(e+1) alike, so the smaller
+// scale is never the worse one. Multiplying by 2^-e is exact, hence so are the
+// codes. A block with a non-finite value gets the NaN scale.
+__device__ __forceinline__ float mx_scale(float amax, uint32_t& scale) {
   const uint32_t bits = __float_as_uint(amax) & 0x7fffffffu;
   int code = (int)(bits >> 23) - 2 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
   code = code < 1 ? 1 : code;
   const bool ok = bits < 0x7f800000u;
-  const float inv = __uint_as_float((uint32_t)(ok ? 254 - code : 0) << 23);
   scale = (uint32_t)(ok ? code : 255);
+  return __uint_as_float((uint32_t)(ok ? 254 - code : 0) << 23);
+}
+__device__ __forceinline__ uint32_t quant8_mx(float* h, float inv) {
   const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
   for (int e = 0; e < 8; e += 2) f2_unpack(f2_mul(f2_pack(h[e], h[e + 1]), inv2), h[e], h[e + 1]);
   return e2m1x8(h);
 }
+
 // Exponent E of a row's scale 2^E: the smallest with amax <= 448 * 6 * 2^E, so
 // that the largest block scale lies in the upper binade of e4m3. 0 for a zero row.
 __device__ __forceinline__ int nv_row_exponent(float amax) {
@@ -219,16 +203,21 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-// Eight values of an NV block with largest magnitude `amax`, in a row of scale
-// 1 / inv_row -> codes and the block's scale byte, amax / 6 in e4m3. The
-// quotient u / s is taken as in quotient(), negated: -u / s keeps the sign of a
-// zero, and the codes' signs are flipped at the end.
-__device__ __forceinline__ uint32_t quant8_nv(float* h, float amax, float inv_row, uint32_t& scale) {
+// NV: scale byte of a block with largest magnitude `amax` in a row of scale
+// 1 / inv_row: amax / 6 in e4m3; its value s and an approximate 1 / s.
+struct NvScale {
+  float s, r;
+};
+__device__ __forceinline__ NvScale nv_scale(float amax, float inv_row, uint32_t& scale) {
   const bool ok = finite_bits(amax);
   scale = ok ? e4m3_code(quotient(amax * inv_row, 6.f, 1.f / 6.f)) : 0x7fu;
   const float s = ok ? e4m3_value(scale) : 0.f;
-  const float r = s > 0.f ? rcp_approx(s) : 0.f;
-  const uint64_t inv2 = f2_pack(inv_row, inv_row), nr2 = f2_pack(-r, -r), s2 = f2_pack(s, s);
+  return {s, s > 0.f ? rcp_approx(s) : 0.f};
+}
+// Eight values u / s (see quotient()), taken as -u / s, which keeps the sign of
+// a zero, and the codes' signs flipped at the end.
+__device__ __forceinline__ uint32_t quant8_nv(float* h, float inv_row, const NvScale& sc) {
+  const uint64_t inv2 = f2_pack(inv_row, inv_row), nr2 = f2_pack(-sc.r, -sc.r), s2 = f2_pack(sc.s, sc.s);
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
     const uint64_t u = f2_mul(f2_pack(h[e], h[e + 1]), inv2);

@@ -250,9 +250,7 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
           continue;
         }
         if (ROT) fwht128_lanes(x[i], lane);
-        am[i] = fabsf(x[i][0]);
-#pragma unroll
-        for (int e = 1; e < 8; ++e) am[i] = max_nan(am[i], fabsf(x[i][e]));
+        am[i] = amax8(x[i]);
         am[i] = max_nan(am[i], __shfl_xor_sync(0xffffffffu, am[i], 1));
         if (HOUT == 2) am[i] = max_nan(am[i], __shfl_xor_sync(0xffffffffu, am[i], 2));
         if (HOUT == 3 && finite_bits(am[i])) top = fmaxf(top, am[i]);
@@ -266,7 +264,13 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
       for (int i = 0; i < CPT; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         uint32_t sc;
-        const uint32_t q = HOUT == 2 ? quant8_mx(x[i], am[i], sc) : quant8_nv(x[i], am[i], pow2_float(-e_row), sc);
+        uint32_t q;
+        if (HOUT == 2) {
+          q = quant8_mx(x[i], mx_scale(am[i], sc));
+        } else {
+          const float inv_row = pow2_float(-e_row);
+          q = quant8_nv(x[i], inv_row, nv_scale(am[i], inv_row, sc));
+        }
         if (c < nchunk) reinterpret_cast<uint32_t*>(a.codes + row * (a.C >> 1))[c] = q;
         // the four scale bytes of an atom's row, gathered from the lanes of 4
         // blocks (MX: 16 lanes, four to a block; NV: 8 lanes, two to a block)
