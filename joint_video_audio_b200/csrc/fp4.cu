@@ -133,17 +133,18 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
     constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
     if (threadIdx.x == 0) row_scale[row] = pow2_float(e_row) * (ROT ? kRot : 1.f);
     uint32_t q[4], sc[2];
-    const float inv_row = pow2_float(-e_row);
+    const int lift = e_row < kNvSmall ? kNvLift : 0;
     float inv = 0.f;
     NvScale nv{};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      if (FMT == kFp4NV && w % 2 == 0) nv = nv_scale(am[w / 2], inv_row, sc[w / 2]);
+      if (FMT == kFp4NV && w % 2 == 0) nv = nv_scale(am[w / 2], e_row, lift, sc[w / 2]);
       if (FMT == kFp4MX && (w == 0 || (ROT && w == 2))) inv = mx_scale(am[w / 2], sc[w / 2]);
       float u[8];
       if (!ROT) unpack_bf16x8(v[w], u);
       float* x = ROT ? h + 8 * w : u;
-      q[w] = FMT == kFp4MX ? quant8_mx(x, inv) : quant8_nv(x, inv_row, nv);
+      if (FMT == kFp4NV && lift) nv_lift8(x);
+      q[w] = FMT == kFp4MX ? quant8_mx(x, inv) : quant8_nv(x, nv);
     }
     uint8_t* crow = codes + row * (K >> 1);
     if (ROT) {

@@ -203,30 +203,38 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
+__device__ __forceinline__ float pow2_float(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 // NV: scale byte of a block with largest magnitude `amax` in a row of scale
-// 1 / inv_row: amax / 6 in e4m3; its value s and an approximate 1 / s.
+// 2^row_exp: amax / 2^row_exp / 6 in e4m3. Returned: the scale times 2^row_exp
+// and an approximate reciprocal of that. Rows of row_exp < kNvSmall, whose
+// reciprocals would overflow, are multiplied by 2^kNvLift first (values, not
+// amax), and `lift` is that.
+constexpr int kNvSmall = -100, kNvLift = 64;
 struct NvScale {
   float s, r;
 };
-__device__ __forceinline__ NvScale nv_scale(float amax, float inv_row, uint32_t& scale) {
+__device__ __forceinline__ NvScale nv_scale(float amax, int row_exp, int lift, uint32_t& scale) {
   const bool ok = finite_bits(amax);
-  scale = ok ? e4m3_code(quotient(amax * inv_row, 6.f, 1.f / 6.f)) : 0x7fu;
+  scale = ok ? e4m3_code(quotient(amax * pow2_float(-row_exp), 6.f, 1.f / 6.f)) : 0x7fu;
   const float s = ok ? e4m3_value(scale) : 0.f;
-  return {s, s > 0.f ? rcp_approx(s) : 0.f};
+  return {s * pow2_float(row_exp + lift), s > 0.f ? rcp_approx(s) * pow2_float(-row_exp - lift) : 0.f};
 }
-// Eight values u / s (see quotient()), taken as -u / s, which keeps the sign of
+// Eight values h / s (see quotient()), taken as -h / s, which keeps the sign of
 // a zero, and the codes' signs flipped at the end.
-__device__ __forceinline__ uint32_t quant8_nv(float* h, float inv_row, const NvScale& sc) {
-  const uint64_t inv2 = f2_pack(inv_row, inv_row), nr2 = f2_pack(-sc.r, -sc.r), s2 = f2_pack(sc.s, sc.s);
+__device__ __forceinline__ uint32_t quant8_nv(float* h, const NvScale& sc) {
+  const uint64_t nr2 = f2_pack(-sc.r, -sc.r), s2 = f2_pack(sc.s, sc.s);
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
-    const uint64_t u = f2_mul(f2_pack(h[e], h[e + 1]), inv2);
+    const uint64_t u = f2_pack(h[e], h[e + 1]);
     const uint64_t nq = f2_mul(u, nr2);
     f2_unpack(f2_fma(f2_fma(nq, s2, u), nr2, nq), h[e], h[e + 1]);
   }
   return e2m1x8(h) ^ 0x88888888u;
 }
-__device__ __forceinline__ float pow2_float(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ void nv_lift8(float* h) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] *= pow2_float(kNvLift);
+}
 __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -268,8 +268,9 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
         if (HOUT == 2) {
           q = quant8_mx(x[i], mx_scale(am[i], sc));
         } else {
-          const float inv_row = pow2_float(-e_row);
-          q = quant8_nv(x[i], inv_row, nv_scale(am[i], inv_row, sc));
+          const int lift = e_row < kNvSmall ? kNvLift : 0;
+          if (lift) nv_lift8(x[i]);
+          q = quant8_nv(x[i], nv_scale(am[i], e_row, lift, sc));
         }
         if (c < nchunk) reinterpret_cast<uint32_t*>(a.codes + row * (a.C >> 1))[c] = q;
         // the four scale bytes of an atom's row, gathered from the lanes of 4
