@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
 }
 
 template <int FMT, bool ROT>
-cudaError_t launch_quant_t(const Fp4QuantArgs& a, cudaStream_t s) {
+cudaError_t launch_quant_t(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
   auto kern = quantize_fp4_kernel<FMT, ROT>;
   const int threads = 32 * ((a.K + 1023) / 1024);
   if (threads > 32 * kMaxRowWarps) return cudaErrorInvalidValue;
@@ -254,12 +254,8 @@ cudaError_t launch_quant_t(const Fp4QuantArgs& a, cudaStream_t s) {
   if (smem > 40 * 1024 &&
       (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
     return e;
-  int dev = 0, sms = 0, per_sm = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return e;
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  const int64_t grid = a.rows < (int64_t)sms * per_sm ? a.rows : (int64_t)sms * per_sm;
+  const int64_t most = (int64_t)num_sms * resident_ctas(threads, 64, smem);
+  const int64_t grid = a.rows < most ? a.rows : most;
   kern<<<(unsigned)grid, threads, smem, s>>>(a.in, a.ld, a.rows, a.K, fp4_katoms(FMT, a.K), stages, a.codes, a.scales,
                                              a.row_scale);
   return cudaGetLastError();
@@ -277,10 +273,10 @@ cudaError_t launch_dequant_t(const Fp4DequantArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, cudaStream_t s) {
+cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
   if (a.rows <= 0) return cudaSuccess;
-  if (a.nv) return a.rotate ? launch_quant_t<kFp4NV, true>(a, s) : launch_quant_t<kFp4NV, false>(a, s);
-  return a.rotate ? launch_quant_t<kFp4MX, true>(a, s) : launch_quant_t<kFp4MX, false>(a, s);
+  if (a.nv) return a.rotate ? launch_quant_t<kFp4NV, true>(a, num_sms, s) : launch_quant_t<kFp4NV, false>(a, num_sms, s);
+  return a.rotate ? launch_quant_t<kFp4MX, true>(a, num_sms, s) : launch_quant_t<kFp4MX, false>(a, num_sms, s);
 }
 
 cudaError_t launch_dequantize_fp4(const Fp4DequantArgs& a, cudaStream_t s) {

@@ -79,7 +79,7 @@ int h3blk_quantize_fp4(const void* in, int64_t ld_in, int rotate, const h3blk_fp
   a.codes = static_cast<uint8_t*>(out->codes);
   a.scales = static_cast<uint8_t*>(out->scales);
   a.row_scale = out->row_scale;
-  return cuda_status(h3::launch_quantize_fp4(a, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(h3::launch_quantize_fp4(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int h3blk_dequantize_fp4(const h3blk_fp4* in, int out_type, void* out, int64_t ld_out, void* stream) {
@@ -201,7 +201,7 @@ int h3blk_sandwich_norm(const h3blk_sandwich* s, void* stream) {
     a.scales = static_cast<uint8_t*>(s->h_fp4->scales);
     a.row_scale = s->h_fp4->row_scale;
   }
-  return cuda_status(h3::launch_sandwich(a, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(h3::launch_sandwich(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

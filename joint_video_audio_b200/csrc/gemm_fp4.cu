@@ -5,15 +5,19 @@
 //
 // gemm_fp4_few_kernel: products of few rows, bound by reading the weight once.
 // The weight rows take the product's M side (128 a CTA), the activations' rows
-// its N side (16 to 128), so no tensor-core row is spent on absent rows.
+// its N side (16 to 128), so no tensor-core row is spent on absent rows. K is
+// split over a cluster of up to eight CTAs when the weight rows alone do not
+// occupy the SMs; the partial sums meet in distributed shared memory, added in
+// the order of K.
 //   warp 0      TMA producer: per stage 256 channels (128 bytes a row) of the
 //               weight rows, of the activation rows, and their block scales
 //   warp 1      TMEM allocator; copies the scale atoms to tensor memory and
 //               issues the products
 //   warps 2..5  epilogue (thread = weight row)
-// The scales' tensor-memory columns are double-buffered per stage of 256
-// channels; a buffer is rewritten once the products that read it have
-// completed.
+// The scales' tensor-memory columns are double-buffered per stage; a buffer is
+// rewritten once the products that read it have completed.
+//
+// gemm_fp4_pair_kernel: products of many rows, see there.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -42,13 +46,80 @@ struct FewCfg {
   static constexpr int kAtoms = atoms_per_stage(FMT);
   static constexpr int kScaleBytes = kAtoms * 512;
   static constexpr int kStageBytes = NW * (kTile + kScaleBytes) + NT * kRowBytes + kScaleBytes;
-  static constexpr int kStages = 4;
+  static constexpr int kStages = NT >= 64 && NW == 1 ? 3 : 4;  // two CTAs of plain products per SM
   static constexpr int kAccCols = NW * NT;
-  static constexpr int kScaleCols = kAtoms * (NW + 1) * 4;  // one buffer
-  static constexpr int kCols = kAccCols + 2 * kScaleCols;
+  static constexpr int kSlotCols = kAtoms * (NW + 1) * 4;
+  static constexpr int kCols = kAccCols + 2 * kSlotCols;
   static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 256;
+  static constexpr int kPerSm = 2 * (kSmem + 1024) <= 228 * 1024 ? 2 : 1;  // resident CTAs
+  static_assert(NW * NT * 512 <= kStages * kStageBytes, "the partial sums take the stages' place");
 };
+
+// A whole stage's tensor work, issued by one lane (see issue_pair_stage): the
+// scale copies (atoms of NW weight tiles and of the activations at sd, sd +
+// kScaleBytes, ..) to the slot at column sc, the four products of 64 channels a
+// weight tile into the accumulators at column d, and the commits.
+#define H3_ARGS                                                                                              \
+  ::"r"(d), "r"(sc), "l"(wd), "l"(xd), "l"(sd), "r"(id0), "r"(id1), "r"(accumulate), "r"(smem_u32(sfree)),   \
+      "r"(smem_u32(empty)), "r"(d + NT)                                                                      \
+      : "memory"
+#define H3_CP(T, X) "add.u32 t, %1, " #T ";\n\tadd.s64 x, %4, " #X ";\n\t" \
+                    "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t], x;\n\t"
+#define H3_MM(OP, D, ID, SA, SB, WK, XK, P)                                                       \
+  "add.u32 t, %1, " #SA ";\n\tadd.u32 u, %1, " #SB ";\n\t"                                      \
+  "add.s64 x, %2, " #WK ";\n\tadd.s64 y, %3, " #XK ";\n\t"                                      \
+  "@e tcgen05.mma.cta_group::1." OP " [" D "], x, y, " ID ", [t], [u], " P ";\n\t"
+#define H3_BEGIN                                                                        \
+  "{\n\t.reg .pred p, q, e;\n\t.reg .b32 t, u;\n\t.reg .b64 x, y;\n\t" H3_ELECT_PRED \
+  "setp.ne.b32 p, %7, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+#define H3_END                                                                                 \
+  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n\t"         \
+  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%9];\n\t}"
+#define H3_NV "kind::mxf4nvf4.block_scale.scale_vec::4X"
+#define H3_MX "kind::mxf4.block_scale.scale_vec::2X"
+template <int FMT, int NT, int NW>
+__device__ __forceinline__ void issue_few_stage(uint32_t d, uint32_t sc, uint64_t wd, uint64_t xd, uint64_t sd,
+                                                uint32_t accumulate, uint64_t* sfree, uint64_t* empty) {
+  constexpr uint32_t id0 = make_idesc_fp4(128, NT, FMT == kFp4MX, 0), id1 = make_idesc_fp4(128, NT, FMT == kFp4MX, 2);
+  static_assert(kTile / 16 == 1024, "the second weight tile's offset below");
+  if (FMT == kFp4NV && NW == 1) {
+    asm volatile(H3_BEGIN                                                            //
+                 H3_CP(0, 0) H3_CP(4, 128) H3_MM(H3_NV, "%0", "%5", 0, 4, 0, 0, "p")      //
+                 H3_CP(8, 32) H3_CP(12, 160) H3_MM(H3_NV, "%0", "%5", 8, 12, 2, 2, "q")   //
+                 H3_CP(16, 64) H3_CP(20, 192) H3_MM(H3_NV, "%0", "%5", 16, 20, 4, 4, "q") //
+                 H3_CP(24, 96) H3_CP(28, 224) H3_MM(H3_NV, "%0", "%5", 24, 28, 6, 6, "q") H3_END H3_ARGS);
+  } else if (FMT == kFp4NV) {
+    asm volatile(H3_BEGIN                                                                                          //
+                 H3_CP(0, 0) H3_CP(4, 128) H3_CP(8, 256) H3_MM(H3_NV, "%0", "%5", 0, 8, 0, 0, "p")                 //
+                 H3_MM(H3_NV, "%10", "%5", 4, 8, 1024, 0, "p")                                                     //
+                 H3_CP(12, 32) H3_CP(16, 160) H3_CP(20, 288) H3_MM(H3_NV, "%0", "%5", 12, 20, 2, 2, "q")           //
+                 H3_MM(H3_NV, "%10", "%5", 16, 20, 1026, 2, "q")                                                   //
+                 H3_CP(24, 64) H3_CP(28, 192) H3_CP(32, 320) H3_MM(H3_NV, "%0", "%5", 24, 32, 4, 4, "q")           //
+                 H3_MM(H3_NV, "%10", "%5", 28, 32, 1028, 4, "q")                                                   //
+                 H3_CP(36, 96) H3_CP(40, 224) H3_CP(44, 352) H3_MM(H3_NV, "%0", "%5", 36, 44, 6, 6, "q")           //
+                 H3_MM(H3_NV, "%10", "%5", 40, 44, 1030, 6, "q") H3_END H3_ARGS);
+  } else if (NW == 1) {
+    asm volatile(H3_BEGIN                                                                                              //
+                 H3_CP(0, 0) H3_CP(4, 64) H3_MM(H3_MX, "%0", "%5", 0, 4, 0, 0, "p")                                    //
+                 H3_MM(H3_MX, "%0", "%6", 0, 4, 2, 2, "q")                                                             //
+                 H3_CP(8, 32) H3_CP(12, 96) H3_MM(H3_MX, "%0", "%5", 8, 12, 4, 4, "q")                                 //
+                 H3_MM(H3_MX, "%0", "%6", 8, 12, 6, 6, "q") H3_END H3_ARGS);
+  } else {
+    asm volatile(H3_BEGIN                                                                                              //
+                 H3_CP(0, 0) H3_CP(4, 64) H3_CP(8, 128) H3_MM(H3_MX, "%0", "%5", 0, 8, 0, 0, "p")                      //
+                 H3_MM(H3_MX, "%10", "%5", 4, 8, 1024, 0, "p") H3_MM(H3_MX, "%0", "%6", 0, 8, 2, 2, "q")               //
+                 H3_MM(H3_MX, "%10", "%6", 4, 8, 1026, 2, "q")                                                         //
+                 H3_CP(12, 32) H3_CP(16, 96) H3_CP(20, 160) H3_MM(H3_MX, "%0", "%5", 12, 20, 4, 4, "q")                //
+                 H3_MM(H3_MX, "%10", "%5", 16, 20, 1028, 4, "q") H3_MM(H3_MX, "%0", "%6", 12, 20, 6, 6, "q")           //
+                 H3_MM(H3_MX, "%10", "%6", 16, 20, 1030, 6, "q") H3_END H3_ARGS);
+  }
+}
+#undef H3_ARGS
+#undef H3_CP
+#undef H3_MM
+#undef H3_BEGIN
+#undef H3_END
 
 template <int FMT, int NT, int NW, typename T>
 __global__ void __launch_bounds__(kFewThreads)
@@ -68,7 +139,10 @@ __global__ void __launch_bounds__(kFewThreads)
   int* abort = reinterpret_cast<int*>(tfull + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * 128, m0 = blockIdx.y * NT;
-  const int num_kb = (p.K + kBlockK - 1) / kBlockK;
+  // this CTA's share of K, in stages
+  const int all_kb = (p.K + kBlockK - 1) / kBlockK;
+  const int split = gridDim.z, part = blockIdx.z;
+  const int kb0 = all_kb * part / split, kb1 = all_kb * (part + 1) / split;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -96,7 +170,7 @@ __global__ void __launch_bounds__(kFewThreads)
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
-      for (int kb = 0; kb < num_kb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1, vabort)) {
           *vabort = 1;
           break;
@@ -133,42 +207,41 @@ __global__ void __launch_bounds__(kFewThreads)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int kb = 0; kb < num_kb; ++kb) {
-      const int buf = kb & 1;
-      if (!mbar_wait_warp(&full[stage], phase, vabort) ||
-          (kb >= 2 && !mbar_wait_warp(&sfree[buf], (uint32_t)((kb >> 1) - 1) & 1, vabort))) {
+    for (int i = 0; i < kb1 - kb0; ++i) {
+      const int buf = i & 1;
+      const uint32_t sfree_parity = ((i >> 1) & 1) ^ 1;
+      const bool r0 = mbar_try_wait(&full[stage], phase), r1 = mbar_try_wait(&sfree[buf], sfree_parity);
+      if (!__all_sync(0xffffffffu, r0 && r1) &&
+          !(mbar_wait_warp(&full[stage], phase, vabort) && mbar_wait_warp(&sfree[buf], sfree_parity, vabort))) {
         if (lane == 0) *vabort = 1;
         ok = false;
         break;
       }
       tc_fence_after();
       const uint32_t st = smem_u32(smem) + (uint32_t)stage * Cfg::kStageBytes;
-      const uint32_t xs = st + NW * kTile, ws0 = xs + NT * kRowBytes, xs0 = ws0 + NW * Cfg::kScaleBytes;
-      const uint32_t sc = tmem + Cfg::kAccCols + buf * Cfg::kScaleCols;
-      const int steps = min(4, (p.K - kb * kBlockK + 63) / 64);
-#pragma unroll
-      for (int a = 0; a < Cfg::kAtoms; ++a) {
-        if (a * fp4_atom_channels(FMT) >= steps * 64) break;
-        const uint32_t col = sc + a * (NW + 1) * 4;
-#pragma unroll
-        for (int i = 0; i < NW; ++i)
-          tmem_cp_scales_w(col + i * 4, scale_atom_desc(ws0 + i * Cfg::kScaleBytes + a * 512));
-        tmem_cp_scales_w(col + NW * 4, scale_atom_desc(xs0 + a * 512));
+      const uint32_t xs = st + NW * kTile, ws0 = xs + NT * kRowBytes;
+      const uint32_t sc = tmem + Cfg::kAccCols + buf * Cfg::kSlotCols;
+      const int left = p.K - (kb0 + i) * kBlockK;
+      if (left > kBlockK - 64) {
+        issue_few_stage<FMT, NT, NW>(tmem, sc, sw128_desc(st, 16), sw128_desc(xs, 16), scale_atom_desc(ws0), i != 0,
+                                     &sfree[buf], &empty[stage]);
+      } else {  // the last stage of a K that does not fill it
+        const int steps = (left + 63) / 64;
+#pragma unroll 1
+        for (int s = 0; s < steps; ++s) {
+          const int a = s * 64 / fp4_atom_channels(FMT);
+          const uint32_t col = sc + a * (NW + 1) * 4;
+          if (s * 64 % fp4_atom_channels(FMT) == 0)
+            for (int j = 0; j <= NW; ++j)
+              tmem_cp_scales_w(col + j * 4, scale_atom_desc(ws0 + j * Cfg::kScaleBytes + a * 512));
+          const uint32_t id = make_idesc_fp4(128, NT, FMT == kFp4MX, FMT == kFp4MX ? (s & 1) * 2 : 0);
+          for (int j = 0; j < NW; ++j)
+            mma_fp4_ss_w<FMT == kFp4NV>(tmem + j * NT, sw128_desc(st + j * kTile + s * 32, 16), sw128_desc(xs + s * 32, 16),
+                                        id, col + j * 4, col + NW * 4, (i | s) != 0);
+        }
+        mma_commit_w(&sfree[buf]);
+        mma_commit_w(&empty[stage]);
       }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (s >= steps) break;
-        const int a = FMT == kFp4NV ? s : s >> 1;
-        const uint32_t id = make_idesc_fp4(128, NT, FMT == kFp4MX, FMT == kFp4MX ? (s & 1) * 2 : 0);
-        const uint32_t col = sc + a * (NW + 1) * 4;
-        const uint64_t xd = sw128_desc(xs + s * 32, 16);
-#pragma unroll
-        for (int i = 0; i < NW; ++i)
-          mma_fp4_ss_w<FMT == kFp4NV>(tmem + i * NT, sw128_desc(st + i * kTile + s * 32, 16), xd, id, col + i * 4,
-                                      col + NW * 4, (kb | s) != 0);
-      }
-      mma_commit_w(&sfree[buf]);
-      mma_commit_w(&empty[stage]);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
@@ -179,37 +252,71 @@ __global__ void __launch_bounds__(kFewThreads)
     mma_commit_w(tfull);
     mbar_wait(tfull, 0, nullptr);
     if (!ok && lane == 0) *vabort = 1;
-  } else {
-    if (mbar_wait(tfull, 0, nullptr) && !*vabort) {
-      tc_fence_after();
-      const int quad = warp & 3;
-      const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16);
-      const int n = n0 + quad * 32 + lane;
-      const bool n_ok = n < p.N;
-      const float rb = n_ok ? __ldg(p.b_row + n) : 0.f;
-      const float ru = NW == 2 && n_ok ? __ldg(p.b_row + p.N + n) : 0.f;
+  }
+  __syncwarp();
+  // ------------------------------------------------------------------ epilogue
+  // sums [NW * NT][128 weight rows] in the place of the stages (every load has
+  // landed and been read); then each CTA of the cluster adds its share of the
+  // activation rows, a warp a row, four weight rows a lane
+  float* sums = reinterpret_cast<float*>(smem);
+  bool good = false;
+  if (warp >= 2) {
+    good = __all_sync(0xffffffffu, mbar_wait(tfull, 0, nullptr) && !*vabort);
+    tc_fence_after();
+    const int quad = warp & 3;
+    const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16);
+    const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
+    if (good) {
 #pragma unroll 1
-      for (int c = 0; c < NT; c += 16) {
-        if (m0 + c >= p.M) break;
-        uint32_t g[16], u[16];
+      for (int c = 0; c < NW * NT; c += 16) {
+        if ((NW == 1 || c < NT ? c : c - NT) >= rows) continue;
+        uint32_t g[16];
         tmem_ld16(acc + c, g);
-        if (NW == 2) tmem_ld16(acc + NT + c, u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int64_t m = m0 + c + i;
-          if (m < p.M && n_ok) {
-            const float ra = __ldg(p.a_row + m);
-            float v = __uint_as_float(g[i]) * ra * rb;
-            if (NW == 2) v = swiglu(v, __uint_as_float(u[i]) * ra * ru);
-            if (sizeof(T) == 2)
-              reinterpret_cast<__nv_bfloat16*>(p.out)[m * p.ld + n] = __float2bfloat16_rn(v);
-            else
-              reinterpret_cast<float*>(p.out)[m * p.ld + n] = v;
-          }
-        }
+        for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + quad * 32 + lane] = __uint_as_float(g[i]);
       }
     }
   }
+  if (split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const int n = n0 + 4 * lane;
+  if (good && n < p.N) {  // N is a multiple of 8
+    const float4 rb = __ldg(reinterpret_cast<const float4*>(p.b_row + n));
+    const float4 ru = NW == 2 ? __ldg(reinterpret_cast<const float4*>(p.b_row + p.N + n)) : rb;
+    const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
+    const uint32_t at = smem_u32(sums) + lane * 16;
+    // the row's sums over the parts, in their order; up to eight loads in flight
+    auto add_parts = [&](int row) {
+      float4 v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < split) v[q] = ld_cluster_f32x4(mapa_shared(at + row * 512, q));
+#pragma unroll
+      for (int q = 1; q < 8; ++q)
+        if (q < split) v[0].x += v[q].x, v[0].y += v[q].y, v[0].z += v[q].z, v[0].w += v[q].w;
+      return v[0];
+    };
+    for (int c = part * 4 + warp - 2; c < rows; c += 4 * split) {
+      const int64_t m = m0 + c;
+      const float ra = __ldg(p.a_row + m);
+      const float4 g = add_parts(c);
+      float4 v = make_float4(g.x * ra * rb.x, g.y * ra * rb.y, g.z * ra * rb.z, g.w * ra * rb.w);
+      if (NW == 2) {
+        const float4 u = add_parts(NT + c);
+        v = make_float4(swiglu(v.x, u.x * ra * ru.x), swiglu(v.y, u.y * ra * ru.y), swiglu(v.z, u.z * ra * ru.z),
+                        swiglu(v.w, u.w * ra * ru.w));
+      }
+      if (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + m * p.ld + n) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      else
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + m * p.ld + n) = v;
+    }
+  }
+  __syncwarp();
+  if (split > 1) cluster_sync();  // no CTA leaves while another reads its sums
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -281,7 +388,6 @@ __device__ __forceinline__ void issue_pair_stage(uint32_t d, uint32_t sc, uint64
       "r"(smem_u32(empty)), "h"((uint16_t)1), "h"((uint16_t)3)                                             \
       : "memory"
   if (FMT == kFp4NV) {
-#define H3_NV "kind::mxf4nvf4.block_scale.scale_vec::4X"
     static_assert(PairCfg<kFp4NV>::kScaleBytes == 128 * 16 && PairCfg<kFp4MX>::kScaleBytes == 64 * 16, "offsets below");
     asm volatile(H3_BLOCK_BEGIN                                                      //
                  H3_CP(0, 0) H3_CP(4, 128) H3_CP(8, 256)                             //
@@ -292,15 +398,12 @@ __device__ __forceinline__ void issue_pair_stage(uint32_t d, uint32_t sc, uint64
                  H3_MM(H3_NV, "%5", 24, 28, 4, "q")                                  //
                  H3_CP(36, 96) H3_CP(40, 224) H3_CP(44, 352)                         //
                  H3_MM(H3_NV, "%5", 36, 40, 6, "q") H3_COMMITS "}" H3_ARGS);
-#undef H3_NV
   } else {
-#define H3_MX "kind::mxf4.block_scale.scale_vec::2X"
     asm volatile(H3_BLOCK_BEGIN                                                      //
                  H3_CP(0, 0) H3_CP(4, 64) H3_CP(8, 128)                              //
                  H3_MM(H3_MX, "%5", 0, 4, 0, "p") H3_MM(H3_MX, "%6", 0, 4, 2, "q")   //
                  H3_CP(12, 32) H3_CP(16, 96) H3_CP(20, 160)                          //
                  H3_MM(H3_MX, "%5", 12, 16, 4, "q") H3_MM(H3_MX, "%6", 12, 16, 6, "q") H3_COMMITS "}" H3_ARGS);
-#undef H3_MX
   }
 #undef H3_ARGS
 }
@@ -308,6 +411,8 @@ __device__ __forceinline__ void issue_pair_stage(uint32_t d, uint32_t sc, uint64
 #undef H3_MM
 #undef H3_COMMITS
 #undef H3_BLOCK_BEGIN
+#undef H3_NV
+#undef H3_MX
 
 struct Tile {
   int m, n;
@@ -666,22 +771,40 @@ struct Maps {
   CUtensorMap a, b, as, bs, out;
 };
 
+constexpr int kMinStages = 2;
+
 template <int FMT, int NT, int NW, typename T>
-cudaError_t launch_few_t(const Fp4GemmArgs& p, const Maps& m, cudaStream_t s) {
+cudaError_t launch_few_t(const Fp4GemmArgs& p, const Maps& m, int num_sms, cudaStream_t s) {
   using Cfg = FewCfg<FMT, NT, NW>;
   auto k = gemm_fp4_few_kernel<FMT, NT, NW, T>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((p.N + 127) / 128, (unsigned)((p.M + NT - 1) / NT));
-  k<<<grid, kFewThreads, Cfg::kSmem, s>>>(m.b, m.a, m.bs, m.as, p);
-  return cudaGetLastError();
+  // K is split while the CTAs still fit on the SMs at once and each keeps
+  // kMinStages stages to stream
+  const int64_t tiles = (p.N + 127) / 128 * ((p.M + NT - 1) / NT);
+  const int stages = (p.K + kBlockK - 1) / kBlockK;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= (int64_t)Cfg::kPerSm * num_sms && stages >= 2 * split * kMinStages) split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.N + 127) / 128, (unsigned)((p.M + NT - 1) / NT), split);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = split;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, m.b, m.a, m.bs, m.as, p);
 }
 
 template <int FMT, int NT>
-cudaError_t launch_few(const Fp4GemmArgs& p, const Maps& m, cudaStream_t s) {
+cudaError_t launch_few(const Fp4GemmArgs& p, const Maps& m, int num_sms, cudaStream_t s) {
   if (p.swiglu)
-    return p.f32 ? launch_few_t<FMT, NT, 2, float>(p, m, s) : launch_few_t<FMT, NT, 2, __nv_bfloat16>(p, m, s);
-  return p.f32 ? launch_few_t<FMT, NT, 1, float>(p, m, s) : launch_few_t<FMT, NT, 1, __nv_bfloat16>(p, m, s);
+    return p.f32 ? launch_few_t<FMT, NT, 2, float>(p, m, num_sms, s) : launch_few_t<FMT, NT, 2, __nv_bfloat16>(p, m, num_sms, s);
+  return p.f32 ? launch_few_t<FMT, NT, 1, float>(p, m, num_sms, s) : launch_few_t<FMT, NT, 1, __nv_bfloat16>(p, m, num_sms, s);
 }
 
 template <int FMT, bool SWIGLU, typename T>
@@ -714,7 +837,7 @@ constexpr int64_t kFewRows = 128;
 template <int FMT>
 cudaError_t launch_fmt(const Fp4GemmArgs& p, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms, cudaStream_t s) {
   Maps m;
-  const bool few = p.M <= kFewRows || num_sms < 2;
+  const bool few = p.M <= kFewRows;
   const int nt = !few ? 128 : p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   const int64_t b_rows = p.swiglu ? 2 * (int64_t)p.N : p.N;
   if (!codes_map(encode, &m.a, p.a_codes, p.M, p.K, nt) || !codes_map(encode, &m.b, p.b_codes, b_rows, p.K, 128) ||
@@ -729,10 +852,10 @@ cudaError_t launch_fmt(const Fp4GemmArgs& p, PFN_cuTensorMapEncodeTiled_v12000 e
                  : launch_pair_t<FMT, false, __nv_bfloat16>(p, m, num_sms, s);
   }
   switch (nt) {
-    case 16: return launch_few<FMT, 16>(p, m, s);
-    case 32: return launch_few<FMT, 32>(p, m, s);
-    case 64: return launch_few<FMT, 64>(p, m, s);
-    default: return launch_few<FMT, 128>(p, m, s);
+    case 16: return launch_few<FMT, 16>(p, m, num_sms, s);
+    case 32: return launch_few<FMT, 32>(p, m, num_sms, s);
+    case 64: return launch_few<FMT, 64>(p, m, num_sms, s);
+    default: return launch_few<FMT, 128>(p, m, num_sms, s);
   }
 }
 

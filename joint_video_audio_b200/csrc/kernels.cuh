@@ -143,7 +143,7 @@ struct Fp4QuantArgs {
   uint8_t* scales;
   float* row_scale;
 };
-cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, cudaStream_t s);
+cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, int num_sms, cudaStream_t s);
 struct Fp4DequantArgs {
   const uint8_t* codes;
   uint8_t* scales;
@@ -186,7 +186,15 @@ struct SandwichArgs {
   uint8_t *codes, *scales;
   float* row_scale;
 };
-cudaError_t launch_sandwich(const SandwichArgs& a, cudaStream_t s);
+cudaError_t launch_sandwich(const SandwichArgs& a, int num_sms, cudaStream_t s);
+// CTAs of a persistent row pass that an SM holds, by threads, registers per
+// thread and shared memory (an estimate: more or fewer only shift the balance).
+inline int resident_ctas(int threads, int regs, size_t smem) {
+  const int by_threads = 2048 / threads, by_regs = 65536 / (threads * regs), by_smem = (int)(224 * 1024 / (smem + 4096));
+  int n = by_threads < by_regs ? by_threads : by_regs;
+  n = by_smem < n ? by_smem : n;
+  return n < 1 ? 1 : n > 32 ? 32 : n;
+}
 
 // ---------------------------------------------------------------- attention
 struct AttnArgs {

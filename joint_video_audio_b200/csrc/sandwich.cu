@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
 }
 
 template <int HOUT, bool ROT, int CPT, int MAXT>
-cudaError_t launch_t(const SandwichArgs& a, cudaStream_t s) {
+cudaError_t launch_t(const SandwichArgs& a, int num_sms, cudaStream_t s) {
   auto kern = sandwich_kernel<HOUT, ROT, CPT, MAXT>;
   const int threads = ((a.C / 8 + CPT - 1) / CPT + 31) / 32 * 32;
   // four rows ahead, up to eight of narrow ones, three of the widest
@@ -298,34 +298,30 @@ cudaError_t launch_t(const SandwichArgs& a, cudaStream_t s) {
   if (smem > 40 * 1024 &&
       (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
     return e;
-  int dev = 0, sms = 0, per_sm = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return e;
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  const int64_t grid = a.rows < (int64_t)sms * per_sm ? a.rows : (int64_t)sms * per_sm;
+  const int64_t most = (int64_t)num_sms * resident_ctas(threads, MAXT == 1024 ? 64 : 88, smem);
+  const int64_t grid = a.rows < most ? a.rows : most;
   kern<<<(unsigned)grid, threads, smem, s>>>(a, stages, HOUT >= 2 ? fp4_katoms(HOUT == 3 ? kFp4NV : kFp4MX, a.C) : 0);
   return cudaGetLastError();
 }
 
 // Thread bounds by width, so that narrow rows leave registers for the vectors.
 template <int HOUT, bool ROT>
-cudaError_t launch_w(const SandwichArgs& a, cudaStream_t s) {
-  if (a.C <= 2048) return launch_t<HOUT, ROT, 1, 256>(a, s);
-  if (a.C <= 5632) return launch_t<HOUT, ROT, 1, 704>(a, s);
-  if (a.C <= 8192) return launch_t<HOUT, ROT, 1, 1024>(a, s);
-  return launch_t<HOUT, ROT, 2, 1024>(a, s);
+cudaError_t launch_w(const SandwichArgs& a, int num_sms, cudaStream_t s) {
+  if (a.C <= 2048) return launch_t<HOUT, ROT, 1, 256>(a, num_sms, s);
+  if (a.C <= 5632) return launch_t<HOUT, ROT, 1, 704>(a, num_sms, s);
+  if (a.C <= 8192) return launch_t<HOUT, ROT, 1, 1024>(a, num_sms, s);
+  return launch_t<HOUT, ROT, 2, 1024>(a, num_sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_sandwich(const SandwichArgs& a, cudaStream_t s) {
+cudaError_t launch_sandwich(const SandwichArgs& a, int num_sms, cudaStream_t s) {
   if (a.rows <= 0) return cudaSuccess;
   if (a.C % 128 || a.C > 16384) return cudaErrorInvalidValue;
-  if (a.norm_table == nullptr) return launch_w<0, false>(a, s);
-  if (a.h) return launch_w<1, false>(a, s);
-  if (a.nv) return a.rotate ? launch_w<3, true>(a, s) : launch_w<3, false>(a, s);
-  return a.rotate ? launch_w<2, true>(a, s) : launch_w<2, false>(a, s);
+  if (a.norm_table == nullptr) return launch_w<0, false>(a, num_sms, s);
+  if (a.h) return launch_w<1, false>(a, num_sms, s);
+  if (a.nv) return a.rotate ? launch_w<3, true>(a, num_sms, s) : launch_w<3, false>(a, num_sms, s);
+  return a.rotate ? launch_w<2, true>(a, num_sms, s) : launch_w<2, false>(a, num_sms, s);
 }
 
 }  // namespace h3

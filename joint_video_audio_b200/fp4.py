@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import ctypes as C
+from functools import lru_cache
 
 import torch
 
@@ -10,33 +11,43 @@ from . import _binding as B
 
 FORMATS = {"mx": B.H3BLK_FP4_MX, "nv": B.H3BLK_FP4_NV}
 _OUT = {torch.bfloat16: B.H3BLK_BF16, torch.float32: B.H3BLK_F32}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _call(fn, name, dev, *args):
-    """fn(*args, stream) on `dev`'s current stream, with `dev` current."""
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+def _call(name, dev, *args):
+    """The library's `name`(*args, stream) on `dev`'s current stream, with `dev` current."""
+    fn, i = getattr(B._lib, name), dev.index
+    if torch.cuda.current_device() == i:
+        st = fn(*args, _raw_stream(i))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(i):
+            st = fn(*args, _raw_stream(i))
     if st != B.H3BLK_OK:
         raise B.H3BlkError(name, st)
 
 
-def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16, cols=None) -> int:
+def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16) -> int:
     """Row stride of a 2-D CUDA tensor with unit column stride; ValueError otherwise."""
-    if not t.is_cuda or t.dim() != 2 or t.dtype != dtype:
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D {dtype} CUDA tensor, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    rows, k = t.shape
-    if cols is not None and k != cols:
-        raise ValueError(f"{name}: expected {cols} columns, got {k}")
-    if k > 1 and t.stride(1) != 1:
+    (rows, k), (ld, unit) = t.shape, t.stride()
+    if unit != 1 and k > 1:
         raise ValueError(f"{name}: its rows are not contiguous")
     if rows < 2:
         return -(-k // 8) * 8
-    if t.stride(0) < k or t.stride(0) % 8:
-        raise ValueError(f"{name}: row stride {t.stride(0)} is not a multiple of 8 of at least {k}")
-    return t.stride(0)
+    if ld < k or ld % 8:
+        raise ValueError(f"{name}: row stride {ld} is not a multiple of 8 of at least {k}")
+    return ld
+
+
+@lru_cache(maxsize=1024)
+def _layout(rows: int, K: int, fmt: str):
+    """(format code, byte lengths, offsets and total of the three parts), every part on a 256-byte boundary."""
+    if fmt not in FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(FORMATS)}, got {fmt!r}")
+    lens = B.h3blk_fp4_bytes(FORMATS[fmt], rows, K)
+    up = [-(-n // 256) * 256 for n in lens]
+    return FORMATS[fmt], lens, (0, up[0], up[0] + up[1]), max(256, sum(up))
 
 
 class Fp4Tensor:
@@ -47,25 +58,18 @@ class Fp4Tensor:
     row_scale  fp32 [rows]
     """
 
+    __slots__ = ("fmt", "shape", "buffer", "device", "c", "_len", "_at")
+
     def __init__(self, rows: int, K: int, fmt: str = "nv", device="cuda"):
-        if fmt not in FORMATS:
-            raise ValueError(f"fmt must be one of {sorted(FORMATS)}, got {fmt!r}")
-        nc, ns, nr = B.h3blk_fp4_bytes(FORMATS[fmt], rows, K)
+        code, self._len, self._at, total = _layout(rows, K, fmt)
         self.fmt, self.shape = fmt, (rows, K)
-        # one buffer; every part starts on a 256-byte boundary
-        self._at = (0, -(-nc // 256) * 256, -(-nc // 256) * 256 + -(-ns // 256) * 256)
-        self._len = (nc, ns, nr)
-        self.buffer = torch.empty(max(256, self._at[2] + nr), dtype=torch.uint8, device=device)
+        self.buffer = torch.empty(total, dtype=torch.uint8, device=device)
+        self.device = self.buffer.device
         p = self.buffer.data_ptr()
-        self.c = B.h3blk_fp4(format=FORMATS[fmt], K=K, rows=rows, codes=p + self._at[0], scales=p + self._at[1],
-                             row_scale=p + self._at[2])
+        self.c = B.h3blk_fp4(code, K, rows, p, p + self._at[1], p + self._at[2])
 
     def _part(self, i):
         return self.buffer[self._at[i]:self._at[i] + self._len[i]]
-
-    @property
-    def device(self):
-        return self.buffer.device
 
     @property
     def codes(self) -> torch.Tensor:
@@ -96,7 +100,7 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "nv", rotate: bool = False, out: Fp
     elif out.fmt != fmt or out.shape != tuple(x.shape) or out.device != x.device:
         raise ValueError(f"out: expected {fmt} {tuple(x.shape)} on {x.device}, got {out}")
     if x.shape[0]:
-        _call(B.h3blk_quantize_fp4, "h3blk_quantize_fp4", x.device, x.data_ptr(), ld, int(rotate), out.c)
+        _call("h3blk_quantize_fp4", x.device, x.data_ptr(), ld, int(rotate), out.c)
     return out
 
 
@@ -107,7 +111,7 @@ def dequantize_fp4(q: Fp4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None 
     out = _output(out, q.shape[0], q.shape[1], dtype, q.device)
     ld = _rows(out, "out", dtype)
     if q.shape[0]:
-        _call(B.h3blk_dequantize_fp4, "h3blk_dequantize_fp4", q.device, q.c, _OUT[dtype], out.data_ptr(), ld)
+        _call("h3blk_dequantize_fp4", q.device, q.c, _OUT[dtype], out.data_ptr(), ld)
     return out
 
 
@@ -131,8 +135,8 @@ def gemm_fp4(a: Fp4Tensor, b: Fp4Tensor, swiglu: bool = False, dtype=torch.bfloa
     out = _output(out, a.shape[0], b.shape[0] // 2 if swiglu else b.shape[0], dtype, a.device)
     ld = _rows(out, "out", dtype)
     if a.shape[0]:
-        _call(B.h3blk_gemm_fp4, "h3blk_gemm_fp4", a.device, a.c, b.c,
-              B.H3BLK_FP4_SWIGLU if swiglu else B.H3BLK_FP4_STORE, _OUT[dtype], out.data_ptr(), ld)
+        _call("h3blk_gemm_fp4", a.device, a.c, b.c, B.H3BLK_FP4_SWIGLU if swiglu else B.H3BLK_FP4_STORE, _OUT[dtype],
+              out.data_ptr(), ld)
     return out
 
 
@@ -152,33 +156,39 @@ def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post
     h3blk_sandwich_norm."""
     if x.dim() != 2 or table.dim() != 4:
         raise ValueError("expected x [rows, hidden] and table [n_tags, n_t, 6, hidden]")
-    n, c = x.shape
-    dev = x.device
+    (n, c), (n_tags, n_t, _, _), dev = x.shape, table.shape, x.device
     if x_out is None:
         x_out = torch.empty_like(x)
     norm_table = (next_table if branch else table) if h is not None else None
-    for name, t, dt, shape in (("x", x, torch.bfloat16, (n, c)), ("y", y, torch.bfloat16, (n, c)),
-                               ("x_out", x_out, torch.bfloat16, (n, c)), ("tag", tag, torch.int32, (n,)),
-                               ("tidx", tidx, torch.int32, (n,)),
-                               ("table", table, torch.float32, (*table.shape[:2], 6, c)),
-                               ("next_table", norm_table, torch.float32, tuple(table.shape)),
-                               ("post_gain", post_gain, torch.bfloat16, (c,))):
-        if t is not None and (not t.is_cuda or t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous()
-                              or t.device != dev):
-            raise ValueError(f"{name}: expected {dt} {shape} contiguous on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    out = None
-    if norm_table is not None:
-        out = torch.empty_like(x) if h == "bf16" else Fp4Tensor(n, c, h, dev)
-    fp4 = out if isinstance(out, Fp4Tensor) else None
-    if rotate and fp4 is None:
+    rows, row, tab = (n, c), (n,), (n_tags, n_t, 6, c)
+    _want("x", x, torch.bfloat16, rows, dev)
+    _want("y", y, torch.bfloat16, rows, dev)
+    _want("x_out", x_out, torch.bfloat16, rows, dev)
+    _want("tag", tag, torch.int32, row, dev)
+    _want("tidx", tidx, torch.int32, row, dev)
+    _want("table", table, torch.float32, tab, dev)
+    if norm_table is not None and norm_table is not table:
+        _want("next_table", norm_table, torch.float32, tab, dev)
+    if post_gain is not None:
+        _want("post_gain", post_gain, torch.bfloat16, (c,), dev)
+    if rotate and h not in FORMATS:
         raise ValueError("rotate is for an h in 4 bits")
-    a = B.h3blk_sandwich(n_rows=n, hidden=c, n_tags=table.shape[0], n_t=table.shape[1], branch=branch,
-                         post_norm=int(post_norm), post_eps=post_eps, norm_eps=norm_eps, branch_scale=branch_scale,
-                         x=x.data_ptr(), y=y.data_ptr(), post_gain=None if post_gain is None else post_gain.data_ptr(),
-                         tag=tag.data_ptr(), tidx=tidx.data_ptr(), mod_table=table.data_ptr(),
-                         norm_table=None if norm_table is None else norm_table.data_ptr(), x_out=x_out.data_ptr(),
-                         h=out.data_ptr() if out is not None and fp4 is None else None,
-                         h_fp4=None if fp4 is None else C.pointer(fp4.c), rotate=int(rotate))
+    out = fp4 = None
+    if norm_table is not None:
+        if h == "bf16":
+            out = torch.empty_like(x)
+        else:
+            out = fp4 = Fp4Tensor(n, c, h, dev)
     if n:
-        _call(B.h3blk_sandwich_norm, "h3blk_sandwich_norm", dev, a)
+        a = B.h3blk_sandwich(n, c, n_tags, n_t, branch, post_norm, post_eps, norm_eps, branch_scale, x.data_ptr(),
+                             y.data_ptr(), None if post_gain is None else post_gain.data_ptr(), tag.data_ptr(),
+                             tidx.data_ptr(), table.data_ptr(), None if norm_table is None else norm_table.data_ptr(),
+                             x_out.data_ptr(), out.data_ptr() if out is not None and fp4 is None else None,
+                             None if fp4 is None else C.pointer(fp4.c), rotate)
+        _call("h3blk_sandwich_norm", dev, a)
     return x_out, out
+
+
+def _want(name, t, dtype, shape, dev):
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {dtype} {shape} contiguous on {dev} (CUDA), got {t.dtype} {tuple(t.shape)} on {t.device}")
