@@ -40,9 +40,9 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// Sum (IS_MAX: max of non-negative values) over the CTA; one barrier. `red`
-// has a slot per warp, of 32, those past the last warp zero, and is written
-// again after another barrier at least.
+// Sums (IS_MAX: maxima of non-negative values) of R rows over the CTA; one
+// barrier. `red` has a slot per warp, of 32, those past the last warp zero, and
+// is written again after another barrier at least.
 template <bool IS_MAX>
 __device__ __forceinline__ float warp_reduce(float v) {
   if (IS_MAX) return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
@@ -50,12 +50,16 @@ __device__ __forceinline__ float warp_reduce(float v) {
   for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
 }
-template <bool IS_MAX>
-__device__ __forceinline__ float cta_reduce(float v, float* red) {
-  v = warp_reduce<IS_MAX>(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+template <bool IS_MAX, int R>
+__device__ __forceinline__ void cta_reduce(float (&v)[R], float (*red)[32]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) v[r] = warp_reduce<IS_MAX>(v[r]);
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int r = 0; r < R; ++r) red[r][threadIdx.x >> 5] = v[r];
   __syncthreads();
-  return warp_reduce<IS_MAX>(red[threadIdx.x & 31]);
+#pragma unroll
+  for (int r = 0; r < R; ++r) v[r] = warp_reduce<IS_MAX>(red[r][threadIdx.x & 31]);
 }
 // Sum of the squares of eight values.
 __device__ __forceinline__ float squares8(const float (&v)[8]) {
@@ -100,14 +104,15 @@ struct Vectors {
   float g[8], sh[8], sc[8];  // gate * gain, shift, 1 + scale
 };
 
-// HOUT: 0 no h, 1 bf16, 2 MX, 3 NV. CPT chunks of eight channels per thread
+// HOUT: 0 no h, 1 bf16, 2 MX, 3 NV. R rows of a key at a time, so that their
+// loads, shuffles and barriers overlap. CPT chunks of eight channels per thread
 // (chunk threadIdx.x + i * blockDim.x); the vectors stay in registers for one
-// chunk and are read per row for two.
-template <int HOUT, bool ROT, int CPT, int MAXT>
+// chunk and are read per row for two (then R is 1).
+template <int HOUT, bool ROT, int CPT, int MAXT, int R>
 __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, int stages, int katoms) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kMaxStages];
-  __shared__ float red[2][3][32];
+  __shared__ float red[2][3][R][32];
   __shared__ int keys[kSortRows];
   __shared__ uint16_t ord[kSortRows];
   __shared__ int fail[2];
@@ -123,7 +128,8 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
     fail[0] = fail[1] = 0;
     fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < 2 * 3 * 32; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+  for (int i = threadIdx.x; i < 2 * 3 * R * 32; i += blockDim.x) (&red[0][0][0][0])[i] = 0.f;
+  const float inv_c = 1.f / (float)a.C;
   Vectors vec[CPT];
   int cur = -2;  // key of the vectors held
   auto load_vectors = [&](int key) {
@@ -183,34 +189,43 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
       fence_proxy_async_smem();  // the slots' last generic reads come before these copies
       for (int i = 0, slot = st; i < stages; ++i, slot = slot + 1 == stages ? 0 : slot + 1) issue(i, slot);
     }
-    for (int k = 0; k < n; ++k) {
-      const int idx = ord[k];
-      const int64_t row = c0 + idx;
-      float(&rd)[3][32] = red[par];
-      const int key = keys[idx];
+    for (int k = 0; k < n;) {
+      const int key = keys[ord[k]];
+      // rows k .. k + cnt - 1, all of this key (a slot past them is zeros)
+      int cnt = 1;
+      if (R == 2 && k + 1 < n && keys[ord[k + 1]] == key) cnt = 2;
+      int64_t at[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) at[r] = (c0 + ord[r < cnt ? k + r : k]) * a.C;
+      float(&rd)[3][R][32] = red[par];
       if (key != cur) {
         if (CPT == 1) load_vectors(key);
         cur = key;
       }
-      if (!mbar_wait(&full[st], phase, nullptr)) fail[par] = 1;
-      float x[CPT][8], y[CPT][8];
-      float ss = 0.f;
+      float x[R][CPT][8], y[R][CPT][8], ss[R];
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        uint4 xv = make_uint4(0, 0, 0, 0), yv = xv;
-        if (c < nchunk) {
-          const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)st * 2 * row_bytes);
-          xv = src[c];
-          yv = src[nchunk + c];
+      for (int r = 0; r < R; ++r) {
+        int slot = st + r, ph = phase;
+        if (slot >= stages) slot -= stages, ph ^= 1;
+        ss[r] = 0.f;
+        if (r < cnt && !mbar_wait(&full[slot], ph, nullptr)) fail[par] = 1;
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          const int c = threadIdx.x + i * blockDim.x;
+          uint4 xv = make_uint4(0, 0, 0, 0), yv = xv;
+          if (r < cnt && c < nchunk) {
+            const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)slot * 2 * row_bytes);
+            xv = src[c];
+            yv = src[nchunk + c];
+          }
+          unpack_bf16x8(xv, x[r][i]);
+          unpack_bf16x8(yv, y[r][i]);
+          if (a.post_norm) ss[r] += squares8(y[r][i]);
         }
-        unpack_bf16x8(xv, x[i]);
-        unpack_bf16x8(yv, y[i]);
-        if (a.post_norm) ss += squares8(y[i]);
       }
-      // a barrier: every thread has read the slot, which is refilled, or the
+      // a barrier: every thread has read the slots, which are refilled, or the
       // CTA stops because a load never landed
-      const float ssy = cta_reduce<false>(ss, rd[0]);
+      cta_reduce<false, R>(ss, rd[0]);
       if (fail[par]) {
         if (threadIdx.x == 0)
           for (int i = k; i < k + stages && i < n; ++i) {
@@ -220,79 +235,95 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
         return;
       }
       if (threadIdx.x == 0) {
-        fail[par ^ 1] = 0;  // every thread passed the last row's check of that flag
+        fail[par ^ 1] = 0;  // every thread passed the last rows' check of that flag
         fence_proxy_async_smem();
         issue(k + stages, st);
+        if (cnt == 2) issue(k + 1 + stages, st + 1 == stages ? 0 : st + 1);
       }
-      if (++st == stages) st = 0, phase ^= 1;
+      k += cnt;
+      st += cnt;
+      if (st >= stages) st -= stages, phase ^= 1;
       par ^= 1;
-      float rp = a.branch_scale;
-      if (a.post_norm) rp *= rsqrtf(ssy / (float)a.C + a.post_eps);
       if (CPT > 1) load_vectors(key);
-      ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (key >= 0)  // (a zero gate times an infinite y would not leave x as it is)
-          scale_fma8(x[i], vec[i].g, rp, y[i], x[i]);
-        if (c < nchunk) reinterpret_cast<uint4*>(a.x_out + row * a.C)[c] = pack8(x[i]);
-        ss += squares8(x[i]);
+      for (int r = 0; r < R; ++r) {
+        float rp = a.branch_scale;
+        if (a.post_norm) rp *= rsqrtf(fmaf(ss[r], inv_c, a.post_eps));
+        ss[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          const int c = threadIdx.x + i * blockDim.x;
+          if (key >= 0)  // (a zero gate times an infinite y would not leave x as it is)
+            scale_fma8(x[r][i], vec[i].g, rp, y[r][i], x[r][i]);
+          if (r < cnt && c < nchunk) reinterpret_cast<uint4*>(a.x_out + at[r])[c] = pack8(x[r][i]);
+          ss[r] += squares8(x[r][i]);
+        }
       }
       if (HOUT == 0) continue;
-      const float rstd = rsqrtf(cta_reduce<false>(ss, rd[1]) / (float)a.C + a.norm_eps);
-      float am[CPT], top = 0.f;
+      cta_reduce<false, R>(ss, rd[1]);
+      float am[R][CPT], top[R];
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        scale_fma8(x[i], x[i], rstd, vec[i].sc, vec[i].sh);
-        if (HOUT == 1) {
-          if (c < nchunk) reinterpret_cast<uint4*>(a.h + row * a.C)[c] = pack8(x[i]);
-          continue;
+      for (int r = 0; r < R; ++r) {
+        const float rstd = rsqrtf(fmaf(ss[r], inv_c, a.norm_eps));
+        top[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          const int c = threadIdx.x + i * blockDim.x;
+          scale_fma8(x[r][i], x[r][i], rstd, vec[i].sc, vec[i].sh);
+          if (HOUT == 1) {
+            if (r < cnt && c < nchunk) reinterpret_cast<uint4*>(a.h + at[r])[c] = pack8(x[r][i]);
+            continue;
+          }
+          if (ROT) fwht128_lanes(x[r][i], lane);
+          float& m = am[r][i];
+          m = amax8(x[r][i]);
+          m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          if (HOUT == 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          if (HOUT == 3 && finite_bits(m)) top[r] = fmaxf(top[r], m);
         }
-        if (ROT) fwht128_lanes(x[i], lane);
-        am[i] = amax8(x[i]);
-        am[i] = max_nan(am[i], __shfl_xor_sync(0xffffffffu, am[i], 1));
-        if (HOUT == 2) am[i] = max_nan(am[i], __shfl_xor_sync(0xffffffffu, am[i], 2));
-        if (HOUT == 3 && finite_bits(am[i])) top = fmaxf(top, am[i]);
       }
-      if (HOUT == 1) continue;
+      if (HOUT <= 1) continue;
+      if (HOUT == 3) cta_reduce<true, R>(top, rd[2]);
       constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
-      int e_row = 0;
-      if (HOUT == 3) e_row = nv_row_exponent(cta_reduce<true>(top, rd[2]));
-      if (threadIdx.x == 0) a.row_scale[row] = pow2_float(e_row) * (ROT ? kRot : 1.f);
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        uint32_t sc;
-        uint32_t q;
-        if (HOUT == 2) {
-          q = quant8_mx(x[i], mx_scale(am[i], sc));
-        } else {
-          const int lift = e_row < kNvSmall ? kNvLift : 0;
-          if (lift) nv_lift8(x[i]);
-          q = quant8_nv(x[i], nv_scale(am[i], e_row, lift, sc));
+      for (int r = 0; r < R; ++r) {
+        const int64_t row = c0 + ord[r < cnt ? k - cnt + r : k - cnt];
+        const int e_row = HOUT == 3 ? nv_row_exponent(top[r]) : 0;
+        const int lift = HOUT == 3 && e_row < kNvSmall ? kNvLift : 0;
+        if (threadIdx.x == 0 && r < cnt) a.row_scale[row] = pow2_float(e_row) * (ROT ? kRot : 1.f);
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          const int c = threadIdx.x + i * blockDim.x;
+          uint32_t sc, q;
+          if (HOUT == 2) {
+            q = quant8_mx(x[r][i], mx_scale(am[r][i], sc));
+          } else {
+            if (lift) nv_lift8(x[r][i]);
+            q = quant8_nv(x[r][i], nv_scale(am[r][i], e_row, lift, sc));
+          }
+          if (r < cnt && c < nchunk) reinterpret_cast<uint32_t*>(a.codes + (at[r] >> 1))[c] = q;
+          // the four scale bytes of an atom's row, gathered from the lanes of 4
+          // blocks (MX: 16 lanes, four to a block; NV: 8 lanes, two to a block)
+          constexpr int kBlk = HOUT == 2 ? 4 : 2;
+          sc <<= 8 * ((lane / kBlk) & 3);
+          sc |= __shfl_xor_sync(0xffffffffu, sc, kBlk);
+          sc |= __shfl_xor_sync(0xffffffffu, sc, 2 * kBlk);
+          if (r < cnt && c < nchunk && lane % (4 * kBlk) == 0)
+            *fp4_scale_word(a.scales, row, katoms, c / (4 * kBlk)) = sc;
         }
-        if (c < nchunk) reinterpret_cast<uint32_t*>(a.codes + row * (a.C >> 1))[c] = q;
-        // the four scale bytes of an atom's row, gathered from the lanes of 4
-        // blocks (MX: 16 lanes, four to a block; NV: 8 lanes, two to a block)
-        constexpr int kBlk = HOUT == 2 ? 4 : 2;
-        sc <<= 8 * ((lane / kBlk) & 3);
-        sc |= __shfl_xor_sync(0xffffffffu, sc, kBlk);
-        sc |= __shfl_xor_sync(0xffffffffu, sc, 2 * kBlk);
-        if (c < nchunk && lane % (4 * kBlk) == 0) *fp4_scale_word(a.scales, row, katoms, c / (4 * kBlk)) = sc;
       }
     }
   }
 }
 
-template <int HOUT, bool ROT, int CPT, int MAXT>
+template <int HOUT, bool ROT, int CPT, int MAXT, int R>
 cudaError_t launch_t(const SandwichArgs& a, int num_sms, cudaStream_t s) {
-  auto kern = sandwich_kernel<HOUT, ROT, CPT, MAXT>;
+  auto kern = sandwich_kernel<HOUT, ROT, CPT, MAXT, R>;
   const int threads = ((a.C / 8 + CPT - 1) / CPT + 31) / 32 * 32;
-  // four rows ahead, up to eight of narrow ones, three of the widest
+  // up to eight rows ahead, three of the widest
   const size_t stage = (size_t)a.C * 4;
   int stages = (int)((a.C <= 2048 ? 32 * 1024 : 192 * 1024) / stage);
-  stages = stages > (a.C <= 2048 ? kMaxStages : 4) ? (a.C <= 2048 ? kMaxStages : 4) : stages;
+  stages = stages > kMaxStages ? kMaxStages : stages;
   const size_t smem = stages * stage;
   cudaError_t e;
   if (smem > 40 * 1024 &&
@@ -307,10 +338,10 @@ cudaError_t launch_t(const SandwichArgs& a, int num_sms, cudaStream_t s) {
 // Thread bounds by width, so that narrow rows leave registers for the vectors.
 template <int HOUT, bool ROT>
 cudaError_t launch_w(const SandwichArgs& a, int num_sms, cudaStream_t s) {
-  if (a.C <= 2048) return launch_t<HOUT, ROT, 1, 256>(a, num_sms, s);
-  if (a.C <= 5632) return launch_t<HOUT, ROT, 1, 704>(a, num_sms, s);
-  if (a.C <= 8192) return launch_t<HOUT, ROT, 1, 1024>(a, num_sms, s);
-  return launch_t<HOUT, ROT, 2, 1024>(a, num_sms, s);
+  if (a.C <= 2048) return launch_t<HOUT, ROT, 1, 256, 2>(a, num_sms, s);
+  if (a.C <= 5632) return launch_t<HOUT, ROT, 1, 704, 2>(a, num_sms, s);
+  if (a.C <= 8192) return launch_t<HOUT, ROT, 1, 1024, 1>(a, num_sms, s);
+  return launch_t<HOUT, ROT, 2, 1024, 1>(a, num_sms, s);
 }
 
 }  // namespace

@@ -11,13 +11,13 @@ from . import _binding as B
 
 FORMATS = {"mx": B.H3BLK_FP4_MX, "nv": B.H3BLK_FP4_NV}
 _OUT = {torch.bfloat16: B.H3BLK_BF16, torch.float32: B.H3BLK_F32}
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _call(name, dev, *args):
     """The library's `name`(*args, stream) on `dev`'s current stream, with `dev` current."""
     fn, i = getattr(B._lib, name), dev.index
-    if torch.cuda.current_device() == i:
+    if _current_device() == i:
         st = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(i):
@@ -190,5 +190,5 @@ def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post
 
 
 def _want(name, t, dtype, shape, dev):
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_cuda or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev.index or not t.is_contiguous():
         raise ValueError(f"{name}: expected {dtype} {shape} contiguous on {dev} (CUDA), got {t.dtype} {tuple(t.shape)} on {t.device}")
