@@ -11,33 +11,34 @@ from . import _binding as B
 
 FORMATS = {"mx": B.H3BLK_FP4_MX, "nv": B.H3BLK_FP4_NV}
 _OUT = {torch.bfloat16: B.H3BLK_BF16, torch.float32: B.H3BLK_F32}
+_quantize, _dequantize = B._lib.h3blk_quantize_fp4, B._lib.h3blk_dequantize_fp4
+_gemm, _sandwich = B._lib.h3blk_gemm_fp4, B._lib.h3blk_sandwich_norm
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _call(name, dev, *args):
-    """The library's `name`(*args, stream) on `dev`'s current stream, with `dev` current."""
-    fn, i = getattr(B._lib, name), dev.index
+def _call(fn, i, *args):
+    """The library call fn(*args, stream) on device i's current stream, with that device current."""
     if _current_device() == i:
         st = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(i):
             st = fn(*args, _raw_stream(i))
-    if st != B.H3BLK_OK:
-        raise B.H3BlkError(name, st)
+    if st:
+        raise B.H3BlkError(fn.__name__, st)
 
 
-def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16) -> int:
-    """Row stride of a 2-D CUDA tensor with unit column stride; ValueError otherwise."""
+def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16):
+    """(rows, columns, row stride) of a 2-D CUDA tensor with unit column stride; ValueError otherwise."""
     if not t.is_cuda or t.dtype != dtype or t.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D {dtype} CUDA tensor, got {t.dtype} {tuple(t.shape)} on {t.device}")
     (rows, k), (ld, unit) = t.shape, t.stride()
     if unit != 1 and k > 1:
         raise ValueError(f"{name}: its rows are not contiguous")
     if rows < 2:
-        return -(-k // 8) * 8
+        return rows, k, -(-k // 8) * 8
     if ld < k or ld % 8:
         raise ValueError(f"{name}: row stride {ld} is not a multiple of 8 of at least {k}")
-    return ld
+    return rows, k, ld
 
 
 @lru_cache(maxsize=1024)
@@ -63,9 +64,9 @@ class Fp4Tensor:
     def __init__(self, rows: int, K: int, fmt: str = "nv", device="cuda"):
         code, self._len, self._at, total = _layout(rows, K, fmt)
         self.fmt, self.shape = fmt, (rows, K)
-        self.buffer = torch.empty(total, dtype=torch.uint8, device=device)
-        self.device = self.buffer.device
-        p = self.buffer.data_ptr()
+        self.buffer = buf = torch.empty(total, dtype=torch.uint8, device=device)
+        self.device = buf.device
+        p = buf.data_ptr()
         self.c = B.h3blk_fp4(code, K, rows, p, p + self._at[1], p + self._at[2])
 
     def _part(self, i):
@@ -94,33 +95,35 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "nv", rotate: bool = False, out: Fp
     e4m3 scales and a power-of-two scale per row. rotate: the block-128 Hadamard
     transform of the W8A8 path first (rotate both operands of a product, or
     neither). h3blk_quantize_fp4."""
-    ld = _rows(x, "x")
+    rows, K, ld = _rows(x, "x")
     if out is None:
-        out = Fp4Tensor(x.shape[0], x.shape[1], fmt, x.device)
-    elif out.fmt != fmt or out.shape != tuple(x.shape) or out.device != x.device:
-        raise ValueError(f"out: expected {fmt} {tuple(x.shape)} on {x.device}, got {out}")
-    if x.shape[0]:
-        _call("h3blk_quantize_fp4", x.device, x.data_ptr(), ld, int(rotate), out.c)
+        out = Fp4Tensor(rows, K, fmt, x.device)
+    elif out.fmt != fmt or out.shape != (rows, K) or out.device != x.device:
+        raise ValueError(f"out: expected {fmt} {(rows, K)} on {x.device}, got {out}")
+    if rows:
+        _call(_quantize, x.get_device(), x.data_ptr(), ld, rotate, out.c)
     return out
 
 
 def dequantize_fp4(q: Fp4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values `q` stands for, bf16 or fp32 [rows, K] (h3blk_dequantize_fp4)."""
-    if dtype not in _OUT:
-        raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
-    out = _output(out, q.shape[0], q.shape[1], dtype, q.device)
-    ld = _rows(out, "out", dtype)
-    if q.shape[0]:
-        _call("h3blk_dequantize_fp4", q.device, q.c, _OUT[dtype], out.data_ptr(), ld)
+    rows, K = q.shape
+    out, ld = _output(out, rows, K, dtype, q.device)
+    if rows:
+        _call(_dequantize, out.get_device(), q.c, _OUT[dtype], out.data_ptr(), ld)
     return out
 
 
 def _output(out, rows, cols, dtype, device):
+    """(output tensor, its row stride), made here where none is given; a
+    stride that is no multiple of 8 (columns that are not) is the library's to refuse."""
+    if dtype not in _OUT:
+        raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
     if out is None:
-        return torch.empty(rows, cols, dtype=dtype, device=device)
+        return torch.empty(rows, cols, dtype=dtype, device=device), cols
     if tuple(out.shape) != (rows, cols) or out.dtype != dtype or out.device != device:
         raise ValueError(f"out: expected {dtype} {(rows, cols)} on {device}, got {out.dtype} {tuple(out.shape)} on {out.device}")
-    return out
+    return out, _rows(out, "out", dtype)[2]
 
 
 def gemm_fp4(a: Fp4Tensor, b: Fp4Tensor, swiglu: bool = False, dtype=torch.bfloat16,
@@ -130,12 +133,10 @@ def gemm_fp4(a: Fp4Tensor, b: Fp4Tensor, swiglu: bool = False, dtype=torch.bfloa
     silu(gate) * up [M, N / 2] (h3blk_gemm_fp4)."""
     if a.fmt != b.fmt or a.shape[1] != b.shape[1] or a.device != b.device:
         raise ValueError(f"operands do not match: {a} and {b}")
-    if dtype not in _OUT:
-        raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
-    out = _output(out, a.shape[0], b.shape[0] // 2 if swiglu else b.shape[0], dtype, a.device)
-    ld = _rows(out, "out", dtype)
-    if a.shape[0]:
-        _call("h3blk_gemm_fp4", a.device, a.c, b.c, B.H3BLK_FP4_SWIGLU if swiglu else B.H3BLK_FP4_STORE, _OUT[dtype],
+    rows, cols = a.shape[0], b.shape[0] // 2 if swiglu else b.shape[0]
+    out, ld = _output(out, rows, cols, dtype, a.device)
+    if rows:
+        _call(_gemm, out.get_device(), a.c, b.c, B.H3BLK_FP4_SWIGLU if swiglu else B.H3BLK_FP4_STORE, _OUT[dtype],
               out.data_ptr(), ld)
     return out
 
@@ -156,7 +157,7 @@ def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post
     h3blk_sandwich_norm."""
     if x.dim() != 2 or table.dim() != 4:
         raise ValueError("expected x [rows, hidden] and table [n_tags, n_t, 6, hidden]")
-    (n, c), (n_tags, n_t, _, _), dev = x.shape, table.shape, x.device
+    (n, c), (n_tags, n_t, _, _), dev = x.shape, table.shape, x.get_device()
     if x_out is None:
         x_out = torch.empty_like(x)
     norm_table = (next_table if branch else table) if h is not None else None
@@ -178,17 +179,17 @@ def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post
         if h == "bf16":
             out = torch.empty_like(x)
         else:
-            out = fp4 = Fp4Tensor(n, c, h, dev)
+            out = fp4 = Fp4Tensor(n, c, h, x.device)
     if n:
         a = B.h3blk_sandwich(n, c, n_tags, n_t, branch, post_norm, post_eps, norm_eps, branch_scale, x.data_ptr(),
                              y.data_ptr(), None if post_gain is None else post_gain.data_ptr(), tag.data_ptr(),
                              tidx.data_ptr(), table.data_ptr(), None if norm_table is None else norm_table.data_ptr(),
                              x_out.data_ptr(), out.data_ptr() if out is not None and fp4 is None else None,
                              None if fp4 is None else C.pointer(fp4.c), rotate)
-        _call("h3blk_sandwich_norm", dev, a)
+        _call(_sandwich, dev, a)
     return x_out, out
 
 
 def _want(name, t, dtype, shape, dev):
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev.index or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {dtype} {shape} contiguous on {dev} (CUDA), got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {dtype} {shape} contiguous on CUDA device {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
