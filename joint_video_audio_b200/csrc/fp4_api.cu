@@ -13,6 +13,7 @@ using h3api::cuda_status;
 constexpr int kMaxChannels = 16384;               // of a row pass, as h3blk_rotate_quantize
 constexpr int kMaxGemmK = 1 << 24;
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kMaxStride = (int64_t)1 << 36;  // a tensor map's strides end at 2^40 bytes
 
 bool known_format(int f) { return f == H3BLK_FP4_MX || f == H3BLK_FP4_NV; }
 
@@ -120,6 +121,7 @@ int h3blk_gemm_fp4(const h3blk_fp4* A, const h3blk_fp4* B, int epilogue, int out
   if (A->K > kMaxGemmK) return H3BLK_ERR_UNSUPPORTED;
   const int64_t N = swiglu ? B->rows / 2 : B->rows;
   if (!out || !aligned16(out) || ld_out < N || ld_out % 8) return H3BLK_ERR_INVALID_ARG;
+  if (ld_out > kMaxStride) return H3BLK_ERR_UNSUPPORTED;
   const size_t bytes = span(A->rows, N, ld_out, out_type == H3BLK_F32 ? 4 : 2);
   if (overlaps_fp4(out, bytes, A) || overlaps_fp4(out, bytes, B)) return H3BLK_ERR_INVALID_ARG;
   int sms = 0;

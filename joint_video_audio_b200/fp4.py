@@ -57,20 +57,24 @@ class Fp4Tensor:
     codes      uint8 [rows, K / 2], two e2m1 codes a byte
     scales     uint8 [..., 512] atoms of 128 rows x 4 block scales
     row_scale  fp32 [rows]
+    rotated    whether the values went through the Hadamard rotation
     """
 
-    __slots__ = ("fmt", "shape", "buffer", "device", "c", "_len", "_at")
+    __slots__ = ("fmt", "shape", "rotated", "buffer", "c", "_len", "_at")
 
     def __init__(self, rows: int, K: int, fmt: str = "nv", device="cuda"):
         code, self._len, self._at, total = _layout(rows, K, fmt)
-        self.fmt, self.shape = fmt, (rows, K)
+        self.fmt, self.shape, self.rotated = fmt, (rows, K), False
         self.buffer = buf = torch.empty(total, dtype=torch.uint8, device=device)
-        self.device = buf.device
         p = buf.data_ptr()
         self.c = B.h3blk_fp4(code, K, rows, p, p + self._at[1], p + self._at[2])
 
     def _part(self, i):
         return self.buffer[self._at[i]:self._at[i] + self._len[i]]
+
+    @property
+    def device(self):
+        return self.buffer.device
 
     @property
     def codes(self) -> torch.Tensor:
@@ -85,7 +89,7 @@ class Fp4Tensor:
         return self._part(2).view(torch.float32)
 
     def __repr__(self):
-        return f"Fp4Tensor({self.shape[0]}, {self.shape[1]}, {self.fmt!r}, {self.device})"
+        return f"Fp4Tensor({self.shape[0]}, {self.shape[1]}, {self.fmt!r}{', rotated' * self.rotated}, {self.device})"
 
 
 def quantize_fp4(x: torch.Tensor, fmt: str = "nv", rotate: bool = False, out: Fp4Tensor | None = None) -> Fp4Tensor:
@@ -93,8 +97,8 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "nv", rotate: bool = False, out: Fp
 
     fmt "mx": blocks of 32 with power-of-two scales; "nv": blocks of 16 with
     e4m3 scales and a power-of-two scale per row. rotate: the block-128 Hadamard
-    transform of the W8A8 path first (rotate both operands of a product, or
-    neither). h3blk_quantize_fp4."""
+    transform of the W8A8 path first (a product takes two rotated operands or
+    two that are not). h3blk_quantize_fp4."""
     rows, K, ld = _rows(x, "x")
     if out is None:
         out = Fp4Tensor(rows, K, fmt, x.device)
@@ -102,6 +106,7 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "nv", rotate: bool = False, out: Fp
         raise ValueError(f"out: expected {fmt} {(rows, K)} on {x.device}, got {out}")
     if rows:
         _call(_quantize, x.get_device(), x.data_ptr(), ld, rotate, out.c)
+    out.rotated = bool(rotate)
     return out
 
 
@@ -131,9 +136,11 @@ def gemm_fp4(a: Fp4Tensor, b: Fp4Tensor, swiglu: bool = False, dtype=torch.bfloa
     """A [M, K] B [N, K]^T of two 4-bit matrices -> bf16 or fp32 [M, N]; with
     swiglu, B holds the gate rows, then the up rows, and the result is
     silu(gate) * up [M, N / 2] (h3blk_gemm_fp4)."""
-    if a.fmt != b.fmt or a.shape[1] != b.shape[1] or a.device != b.device:
+    (rows, K), (cols, Kb) = a.shape, b.shape
+    if a.fmt != b.fmt or K != Kb or a.rotated != b.rotated or a.device != b.device:
         raise ValueError(f"operands do not match: {a} and {b}")
-    rows, cols = a.shape[0], b.shape[0] // 2 if swiglu else b.shape[0]
+    if swiglu:
+        cols //= 2
     out, ld = _output(out, rows, cols, dtype, a.device)
     if rows:
         _call(_gemm, out.get_device(), a.c, b.c, B.H3BLK_FP4_SWIGLU if swiglu else B.H3BLK_FP4_STORE, _OUT[dtype],
@@ -172,6 +179,8 @@ def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post
         _want("next_table", norm_table, torch.float32, tab, dev)
     if post_gain is not None:
         _want("post_gain", post_gain, torch.bfloat16, (c,), dev)
+    if h is not None and h != "bf16" and h not in FORMATS:
+        raise ValueError(f"h must be None, 'bf16', 'mx' or 'nv', got {h!r}")
     if rotate and h not in FORMATS:
         raise ValueError("rotate is for an h in 4 bits")
     out = fp4 = None
@@ -180,6 +189,7 @@ def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post
             out = torch.empty_like(x)
         else:
             out = fp4 = Fp4Tensor(n, c, h, x.device)
+            fp4.rotated = bool(rotate)
     if n:
         a = B.h3blk_sandwich(n, c, n_tags, n_t, branch, post_norm, post_eps, norm_eps, branch_scale, x.data_ptr(),
                              y.data_ptr(), None if post_gain is None else post_gain.data_ptr(), tag.data_ptr(),

@@ -64,7 +64,7 @@ def test_dequantize_refusals(out, ld, typ, status):
     ({}, {}, {}, OK), ({"rows": 1}, {"rows": 8}, {"ld": 8}, OK), ({}, {"rows": 512}, {"epi": 1, "ld": 256}, OK),
     ({}, {"K": 288}, {}, BAD), ({}, {"format": 0}, {}, BAD), ({}, {"rows": 0}, {}, BAD), ({}, {"rows": 4}, {}, UNS),
     ({}, {"rows": 384}, {"epi": 1}, UNS), ({}, {}, {"epi": 2}, BAD), ({}, {}, {"typ": 2}, BAD), ({}, {}, {"out": 0}, BAD),
-    ({}, {}, {"out": p(1) + 4}, BAD), ({}, {}, {"ld": 120}, BAD), ({}, {}, {"ld": 132}, BAD), ({}, {}, {"out": p(2)}, BAD),
+    ({}, {}, {"out": p(1) + 4}, BAD), ({}, {}, {"ld": 120}, BAD), ({}, {}, {"ld": 132}, BAD), ({}, {}, {"out": p(2)}, BAD), ({"rows": 1}, {}, {"ld": (1 << 36) + 8}, UNS),
     ({}, {}, {"out": p(3) + (1 << 34)}, BAD), ({"codes": 0}, {}, {}, BAD), ({}, {"row_scale": p(3) + 4}, {}, BAD),
 ])
 def test_gemm_refusals(a, b, kw, status):
@@ -114,6 +114,13 @@ def test_python_refusals():
         j.gemm_fp4(a, b)
     with pytest.raises(ValueError):
         j.dequantize_fp4(a, torch.float16)
+    c, d = j.Fp4Tensor(4, 256, "nv", device="cpu"), j.Fp4Tensor(8, 256, "nv", device="cpu")
+    d.rotated = True
+    with pytest.raises(ValueError, match="rotated"):
+        j.gemm_fp4(c, d)
     i = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError):
         j.sandwich_norm(cpu, cpu, i, i, torch.zeros(4, 2, 6, 256))
+    for kw in ({"h": "fp8"}, {"h": "bf16", "rotate": True}, {"h": None, "rotate": True}):
+        with pytest.raises(ValueError):
+            j.sandwich_norm(cpu, cpu, i, i, torch.zeros(4, 2, 6, 256), **kw)

@@ -69,6 +69,15 @@ def test_quantize_every_bf16_value(j, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("rows,k", [(20001, 64), (3000, 1056), (1500, 2080), (700, 4128)])
+def test_quantize_more_rows_than_ctas(j, fmt, rows, k):
+    """Every CTA takes many rows, its ring goes round several times."""
+    x = _rows(rows, k, k)
+    x[rows // 3, 40] = float("nan")
+    assert_same_bits(j.quantize_fp4(x.cuda(), fmt), o.quantize(x, fmt))
+
+
+@pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("rows,k", [(3, 128), (40, 5376), (1, 1152), (2, 16384)])
 def test_quantize_rotated_bits(j, fmt, rows, k):
     """Integers of up to 8 bits: their sums of 128 are exact in fp32, so the
@@ -138,6 +147,16 @@ def test_gemm(j, fmt, dtype, m, n, k):
     y = o.product(a, b)
     got = j.gemm_fp4(qa, qb, dtype=dtype).double().cpu().numpy()
     assert np.all(np.abs(got - y) <= _tolerance(a, b, dtype, y))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("m,n,k", [(2600, 2000, 256), (2300, 2600, 160), (2600, 2600, 96), (200, 5376, 512), (140, 72, 1024)])
+def test_gemm_waves(j, fmt, m, n, k):
+    """More tiles than the SMs take at once, the rest in quarters, halves or whole; fewer tiles than SMs."""
+    qa, qb, a, b = _operands(j, m, n, k, fmt)
+    y = o.product(a, b)
+    got = j.gemm_fp4(qa, qb).double().cpu().numpy()
+    assert np.all(np.abs(got - y) <= _tolerance(a, b, torch.bfloat16, y))
 
 
 @pytest.mark.parametrize("fmt", FMT)
