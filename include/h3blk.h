@@ -311,7 +311,10 @@ H3BLK_API int h3blk_dequantize_fp4(const h3blk_fp4* in, int out_type, void* out,
  *   H3BLK_FP4_SWIGLU  out[m, n] = silu(A[m] . B[n]) * (A[m] . B[F + n])
  *                     [A->rows, F], F = B->rows / 2 (the layout of w13)
  * A->rows may be 0. UNSUPPORTED unless the output's columns are a multiple of
- * 8 (STORE) or 128 (SWIGLU). `out` must not overlap the operands. */
+ * 8 (STORE) or 128 (SWIGLU). `out` must not overlap the operands. Both operands
+ * are rotated or neither is (not checked here). As with the other kernel-level
+ * calls, a pipeline wait that runs out (2 s) ends the kernel with its output
+ * incomplete, and nothing reports it. */
 #define H3BLK_FP4_STORE 0
 #define H3BLK_FP4_SWIGLU 1
 H3BLK_API int h3blk_gemm_fp4(const h3blk_fp4* A, const h3blk_fp4* B, int epilogue, int out_type, void* out,

@@ -124,6 +124,8 @@ def _output(out, rows, cols, dtype, device):
     stride that is no multiple of 8 (columns that are not) is the library's to refuse."""
     if dtype not in _OUT:
         raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    if device.type != "cuda":
+        raise ValueError(f"expected operands on a CUDA device, got {device}")
     if out is None:
         return torch.empty(rows, cols, dtype=dtype, device=device), cols
     if tuple(out.shape) != (rows, cols) or out.dtype != dtype or out.device != device:

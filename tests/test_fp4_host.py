@@ -115,6 +115,9 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         j.dequantize_fp4(a, torch.float16)
     c, d = j.Fp4Tensor(4, 256, "nv", device="cpu"), j.Fp4Tensor(8, 256, "nv", device="cpu")
+    for call in (lambda: j.gemm_fp4(c, d), lambda: j.dequantize_fp4(c)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
     d.rotated = True
     with pytest.raises(ValueError, match="rotated"):
         j.gemm_fp4(c, d)

@@ -88,6 +88,24 @@ def test_quantize_rotated_bits(j, fmt, rows, k):
 
 
 @pytest.mark.parametrize("fmt", FMT)
+def test_quantize_rotated_non_finite(j, fmt):
+    """An infinity or a NaN takes its 128 channels and nothing else."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.randint(-64, 65, (5, 1280), generator=g).to(torch.bfloat16)
+    y = x.clone()
+    y[1, 300], y[3, 1279] = float("inf"), float("nan")
+    y[3, 1100], y[4, 0], y[4, 1] = float("-inf"), float("inf"), float("-inf")
+    q = j.quantize_fp4(y.cuda(), fmt, rotate=True)
+    v = j.dequantize_fp4(q, torch.float32).double().cpu().numpy()
+    bad = np.zeros((5, 10), bool)
+    bad[1, 2], bad[3, 9], bad[3, 8], bad[4, 0] = True, True, True, True
+    assert np.array_equal(np.isnan(v).reshape(5, 10, 128), np.repeat(bad[..., None], 128, 2))
+    c, s, r, _ = o.quantize(y, fmt, True)
+    ok = np.repeat(~bad, 128, 1)
+    np.testing.assert_allclose(v[ok], o.values(c, s, r, fmt)[ok], rtol=2.0 ** -22)
+
+
+@pytest.mark.parametrize("fmt", FMT)
 def test_quantize_strided_rows_and_pads(j, fmt):
     """Rows inside a wider buffer; the scale bytes past K are finite, those of
     rows past the last are left as they were."""
