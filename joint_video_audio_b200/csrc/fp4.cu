@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
     if (++st == stages) st = 0, phase ^= 1;
     int e_row = 0;
     if (FMT == kFp4NV) {
-      for (int i = 0; i < warps; ++i) top = fmaxf(top, red[par][i]);
-      e_row = nv_row_exponent(top);
+      top = lane < warps ? red[par][lane] : 0.f;
+      e_row = nv_row_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
     }
     constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
     if (threadIdx.x == 0) row_scale[row] = pow2_float(e_row) * (ROT ? kRot : 1.f);
