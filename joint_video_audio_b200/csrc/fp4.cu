@@ -47,6 +47,11 @@ __device__ __forceinline__ uint4 group_transpose(const uint32_t (&w)[4], int lan
 // the row's largest magnitude before its first code: the barrier that hands a
 // slot back for refilling is also that reduction's.
 //
+// Measured (32768 x 14336, 2.53 / 2.56 bytes a value): MX 205 us (5.8 TB/s, 89 %
+// of the copy rate), MX rotated 209 us, NV 219 us, NV rotated 285 us, the last
+// two bound by issue (2.6-2.7 instructions a cycle). One row per CTA at a time
+// without the ring took 240, 338, 379 and 467 us.
+//
 // A lane works on 32 channels: unrotated the 32 from 32 threadIdx.x (an MX
 // block, two NV blocks; its 16-byte reads of the row in an order that gives
 // each eight lanes distinct banks), rotated as fwht128_warp leaves them.
@@ -189,6 +194,9 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
   }
 }
 
+// 32 channels a lane, read as one 16-byte piece of codes and transposed among
+// four lanes so that the values leave in 64-byte runs. Measured (32768 x 14336
+// -> bf16): 186 us MX, 192 us NV, 97 and 95 % of the copy rate.
 template <int FMT, typename T>
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __restrict__ codes, uint8_t* scales,
                                                            const float* __restrict__ row_scale, int64_t rows, int K,

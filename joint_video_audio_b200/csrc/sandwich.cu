@@ -15,7 +15,12 @@
 // them. So a persistent CTA takes a contiguous slice of the rows, visits them
 // grouped by (tag, tidx), and a thread keeps its eight channels' vectors in
 // registers while the key stays. Rows arrive by bulk copies issued several
-// rows ahead; a row's two or three reductions are one barrier each.
+// rows ahead; two rows of a key are worked on together, and their two or three
+// reductions are one barrier each.
+//
+// Measured (32768 x 5376): bf16 h 242 us (5.8 TB/s, 89 % of the copy rate), MX h
+// 295 us and NV h 336 us (bound by issue, 2.3 instructions a cycle). One row at a
+// time took 287 us, vectors read per row 557 us.
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"
