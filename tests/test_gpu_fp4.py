@@ -284,3 +284,23 @@ def test_empty_operands(j):
     w = j.quantize_fp4(torch.zeros(64, 128, dtype=torch.bfloat16, device="cuda"), "mx")
     q = j.quantize_fp4(torch.zeros(0, 128, dtype=torch.bfloat16, device="cuda"), "mx")
     assert j.dequantize_fp4(q).shape == (0, 128) and j.gemm_fp4(q, w).shape == (0, 64)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_offsets_past_32_bits(j, fmt):
+    """270 repeats of 1000 rows: the values' and the product's indices pass 2^31
+    and their bytes 2^32, the codes' bytes 2^31. Every repeat gives the bits of
+    the first, and those of the 1000 rows alone."""
+    reps, rows, k, n = 270, 1000, 16384, 8192
+    assert reps * rows * k // 2 > 2 ** 31 < reps * rows * n
+    base = _rows(rows, k, 21).cuda()
+    one, q = j.quantize_fp4(base, fmt), j.quantize_fp4(base.repeat(reps, 1), fmt)
+    assert torch.equal(q.codes.view(reps, -1), one.codes.view(1, -1).expand(reps, -1))
+    assert torch.equal(q.row_scale.view(reps, -1), one.row_scale.expand(reps, -1))
+    v, first = j.dequantize_fp4(q), j.dequantize_fp4(one)
+    assert torch.equal(v.view(reps, -1), first.view(1, -1).expand(reps, -1))
+    del v
+    g = torch.Generator().manual_seed(22)
+    w = j.quantize_fp4((torch.randn(n, k, generator=g) / 128).to(torch.bfloat16).cuda(), fmt)
+    y, first = j.gemm_fp4(q, w), j.gemm_fp4(one, w)
+    assert torch.equal(y.view(reps, -1), first.view(1, -1).expand(reps, -1))

@@ -194,3 +194,21 @@ def test_feed_forward_half_of_the_block_in_4_bits(j, fmt, rotate, n):
         again = step()
     graph.replay()
     assert torch.equal(again[5], x2) and torch.equal(again[6], h2)
+
+
+@pytest.mark.parametrize("h", ["bf16", "mx"])
+def test_offsets_past_32_bits(j, h):
+    """420 repeats of 1000 rows, more than 2^31 values in each tensor: every
+    repeat gives the bits of the first, and those of the 1000 rows alone."""
+    reps, n, c = 420, 1000, 5376
+    assert reps * n * c > 2 ** 31
+    d = _case(n, c, 31)
+    x1, h1 = _run(j, d, 0, True, h=h)
+    long = dict(d, **{k: d[k].cuda().repeat(reps, *[1] * (d[k].dim() - 1)) for k in ("x", "y", "tag", "tidx")})
+    xl, hl = _run(j, long, 0, True, h=h)
+    assert torch.equal(xl.view(reps, -1), x1.view(1, -1).expand(reps, -1))
+    if h == "bf16":
+        assert torch.equal(hl.view(reps, -1), h1.view(1, -1).expand(reps, -1))
+    else:
+        assert torch.equal(hl.codes.view(reps, -1), h1.codes.view(1, -1).expand(reps, -1))
+        assert torch.equal(hl.row_scale.view(reps, -1), h1.row_scale.expand(reps, -1))
