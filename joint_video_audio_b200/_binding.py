@@ -136,10 +136,11 @@ def _load():
         "h3blk_gemm_s8_s32": (i32, [i64, i32, i32, vp, vp, vp, vp]),
         "h3blk_gemm_bf16": (i32, [i64, i32, i32, vp, vp, vp, vp]),
         "h3blk_fp4_bytes": (i32, [i32, i64, i32, C.POINTER(sz), C.POINTER(sz), C.POINTER(sz)]),
-        "h3blk_quantize_fp4": (i32, [vp, i64, i32, C.POINTER(h3blk_fp4), vp]),
-        "h3blk_dequantize_fp4": (i32, [C.POINTER(h3blk_fp4), i32, vp, i64, vp]),
-        "h3blk_gemm_fp4": (i32, [C.POINTER(h3blk_fp4), C.POINTER(h3blk_fp4), i32, i32, vp, i64, vp]),
-        "h3blk_sandwich_norm": (i32, [C.POINTER(h3blk_sandwich), vp]),
+        # structs by address: C.byref(struct), an int, or the packed bytes
+        "h3blk_quantize_fp4": (i32, [vp, i64, i32, vp, vp]),
+        "h3blk_dequantize_fp4": (i32, [vp, i32, vp, i64, vp]),
+        "h3blk_gemm_fp4": (i32, [vp, vp, i32, i32, vp, i64, vp]),
+        "h3blk_sandwich_norm": (i32, [vp, vp]),
         "h3blk_error_string": (C.c_char_p, [i32]),
         "h3blk_version": (i32, []),
         "h3blk_set_kernel_events": (i32, [vp, C.POINTER(vp), i32]),
@@ -274,21 +275,25 @@ def h3blk_fp4_bytes(fmt, rows, K) -> tuple[int, int, int]:
     return a.value, b.value, c.value
 
 
+def _ref(struct):
+    return None if struct is None else C.byref(struct)
+
+
 def h3blk_quantize_fp4(in_bf16, ld_in, rotate, out: h3blk_fp4, stream) -> int:
     """Raw call (pointers are ints); returns the status code."""
-    return _lib.h3blk_quantize_fp4(in_bf16, ld_in, rotate, out, stream)
+    return _lib.h3blk_quantize_fp4(in_bf16, ld_in, rotate, _ref(out), stream)
 
 
 def h3blk_dequantize_fp4(q: h3blk_fp4, out_type, out, ld_out, stream) -> int:
-    return _lib.h3blk_dequantize_fp4(q, out_type, out, ld_out, stream)
+    return _lib.h3blk_dequantize_fp4(_ref(q), out_type, out, ld_out, stream)
 
 
 def h3blk_gemm_fp4(a: h3blk_fp4, b: h3blk_fp4, epilogue, out_type, out, ld_out, stream) -> int:
-    return _lib.h3blk_gemm_fp4(a, b, epilogue, out_type, out, ld_out, stream)
+    return _lib.h3blk_gemm_fp4(_ref(a), _ref(b), epilogue, out_type, out, ld_out, stream)
 
 
 def h3blk_sandwich_norm(args: h3blk_sandwich, stream) -> int:
-    return _lib.h3blk_sandwich_norm(args, stream)
+    return _lib.h3blk_sandwich_norm(_ref(args), stream)
 
 
 def h3blk_set_kernel_events(handle, events) -> None:

@@ -21,26 +21,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// A 4 x 4 transpose of words among four neighbouring lanes: lane q of them gets
-// word q of each, in lane order.
-__device__ __forceinline__ uint4 group_transpose(const uint32_t (&w)[4], int lane) {
-  const bool o1 = lane & 1, o2 = lane & (2);
-  uint32_t a0 = w[0], a1 = w[1], a2 = w[2], a3 = w[3];
-  uint32_t s0 = __shfl_xor_sync(0xffffffffu, o1 ? a0 : a1, 1);
-  uint32_t s1 = __shfl_xor_sync(0xffffffffu, o1 ? a2 : a3, 1);
-  a0 = o1 ? s0 : a0;
-  a2 = o1 ? s1 : a2;
-  a1 = o1 ? a1 : s0;
-  a3 = o1 ? a3 : s1;
-  s0 = __shfl_xor_sync(0xffffffffu, o2 ? a0 : a2, 2);
-  s1 = __shfl_xor_sync(0xffffffffu, o2 ? a1 : a3, 2);
-  a0 = o2 ? s0 : a0;
-  a1 = o2 ? s1 : a1;
-  a2 = o2 ? a2 : s0;
-  a3 = o2 ? a3 : s1;
-  return make_uint4(a0, a1, a2, a3);
-}
-
 // Persistent CTAs of as many warps as a row of 1024 channels each takes, one
 // row at a time (row = blockIdx.x + i * gridDim.x), four lanes to a block of
 // 128 channels. Rows arrive by bulk copies issued `stages` rows ahead. NV needs
@@ -192,6 +172,26 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
       }
     }
   }
+}
+
+// A 4 x 4 transpose of words among four neighbouring lanes: lane q of them gets
+// word q of each, in lane order.
+__device__ __forceinline__ uint4 group_transpose(const uint32_t (&w)[4], int lane) {
+  const bool o1 = lane & 1, o2 = lane & 2;
+  uint32_t a0 = w[0], a1 = w[1], a2 = w[2], a3 = w[3];
+  uint32_t s0 = __shfl_xor_sync(0xffffffffu, o1 ? a0 : a1, 1);
+  uint32_t s1 = __shfl_xor_sync(0xffffffffu, o1 ? a2 : a3, 1);
+  a0 = o1 ? s0 : a0;
+  a2 = o1 ? s1 : a2;
+  a1 = o1 ? a1 : s0;
+  a3 = o1 ? a3 : s1;
+  s0 = __shfl_xor_sync(0xffffffffu, o2 ? a0 : a2, 2);
+  s1 = __shfl_xor_sync(0xffffffffu, o2 ? a1 : a3, 2);
+  a0 = o2 ? s0 : a0;
+  a1 = o2 ? s1 : a1;
+  a2 = o2 ? a2 : s0;
+  a3 = o2 ? a3 : s1;
+  return make_uint4(a0, a1, a2, a3);
 }
 
 // 32 channels a lane, read as one 16-byte piece of codes and transposed among

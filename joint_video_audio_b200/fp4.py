@@ -2,8 +2,9 @@
 (no arithmetic here): include/h3blk.h states the formats and the formulas."""
 from __future__ import annotations
 
-import ctypes as C
+from ctypes import addressof
 from functools import lru_cache
+from struct import Struct
 
 import torch
 
@@ -13,6 +14,8 @@ FORMATS = {"mx": B.H3BLK_FP4_MX, "nv": B.H3BLK_FP4_NV}
 _OUT = {torch.bfloat16: B.H3BLK_BF16, torch.float32: B.H3BLK_F32}
 _quantize, _dequantize = B._lib.h3blk_quantize_fp4, B._lib.h3blk_dequantize_fp4
 _gemm, _sandwich = B._lib.h3blk_gemm_fp4, B._lib.h3blk_sandwich_norm
+# h3blk_sandwich in its C layout: packing it takes 0.4 us, filling the ctypes structure 1.8 us
+_pack_sandwich = Struct("@qiiiiifffPPPPPPPPPPi0P").pack
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
@@ -60,17 +63,19 @@ class Fp4Tensor:
     rotated    whether the values went through the Hadamard rotation
     """
 
-    __slots__ = ("fmt", "shape", "rotated", "buffer", "c", "_len", "_at")
+    __slots__ = ("fmt", "shape", "rotated", "buffer", "c", "ref")
 
     def __init__(self, rows: int, K: int, fmt: str = "nv", device="cuda"):
-        code, self._len, self._at, total = _layout(rows, K, fmt)
+        code, _, (_, scales, row_scale), total = _layout(rows, K, fmt)
         self.fmt, self.shape, self.rotated = fmt, (rows, K), False
         self.buffer = buf = torch.empty(total, dtype=torch.uint8, device=device)
         p = buf.data_ptr()
-        self.c = B.h3blk_fp4(code, K, rows, p, p + self._at[1], p + self._at[2])
+        self.c = c = B.h3blk_fp4(code, K, rows, p, p + scales, p + row_scale)
+        self.ref = addressof(c)
 
     def _part(self, i):
-        return self.buffer[self._at[i]:self._at[i] + self._len[i]]
+        _, lens, at, _ = _layout(*self.shape, self.fmt)
+        return self.buffer[at[i]:at[i] + lens[i]]
 
     @property
     def device(self):
@@ -105,7 +110,7 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "nv", rotate: bool = False, out: Fp
     elif out.fmt != fmt or out.shape != (rows, K) or out.device != x.device:
         raise ValueError(f"out: expected {fmt} {(rows, K)} on {x.device}, got {out}")
     if rows:
-        _call(_quantize, x.get_device(), x.data_ptr(), ld, rotate, out.c)
+        _call(_quantize, x.get_device(), x.data_ptr(), ld, rotate, out.ref)
     out.rotated = bool(rotate)
     return out
 
@@ -115,7 +120,7 @@ def dequantize_fp4(q: Fp4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None 
     rows, K = q.shape
     out, ld = _output(out, rows, K, dtype, q.device)
     if rows:
-        _call(_dequantize, out.get_device(), q.c, _OUT[dtype], out.data_ptr(), ld)
+        _call(_dequantize, out.get_device(), q.ref, _OUT[dtype], out.data_ptr(), ld)
     return out
 
 
@@ -145,7 +150,7 @@ def gemm_fp4(a: Fp4Tensor, b: Fp4Tensor, swiglu: bool = False, dtype=torch.bfloa
         cols //= 2
     out, ld = _output(out, rows, cols, dtype, a.device)
     if rows:
-        _call(_gemm, out.get_device(), a.c, b.c, B.H3BLK_FP4_SWIGLU if swiglu else B.H3BLK_FP4_STORE, _OUT[dtype],
+        _call(_gemm, out.get_device(), a.ref, b.ref, B.H3BLK_FP4_SWIGLU if swiglu else B.H3BLK_FP4_STORE, _OUT[dtype],
               out.data_ptr(), ld)
     return out
 
@@ -193,11 +198,10 @@ def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post
             out = fp4 = Fp4Tensor(n, c, h, x.device)
             fp4.rotated = bool(rotate)
     if n:
-        a = B.h3blk_sandwich(n, c, n_tags, n_t, branch, post_norm, post_eps, norm_eps, branch_scale, x.data_ptr(),
-                             y.data_ptr(), None if post_gain is None else post_gain.data_ptr(), tag.data_ptr(),
-                             tidx.data_ptr(), table.data_ptr(), None if norm_table is None else norm_table.data_ptr(),
-                             x_out.data_ptr(), out.data_ptr() if out is not None and fp4 is None else None,
-                             None if fp4 is None else C.pointer(fp4.c), rotate)
+        a = _pack_sandwich(n, c, n_tags, n_t, branch, post_norm, post_eps, norm_eps, branch_scale, x.data_ptr(),
+                           y.data_ptr(), 0 if post_gain is None else post_gain.data_ptr(), tag.data_ptr(), tidx.data_ptr(),
+                           table.data_ptr(), 0 if norm_table is None else norm_table.data_ptr(), x_out.data_ptr(),
+                           0 if out is None or fp4 is not None else out.data_ptr(), 0 if fp4 is None else fp4.ref, rotate)
         _call(_sandwich, dev, a)
     return x_out, out
 

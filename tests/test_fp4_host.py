@@ -96,6 +96,17 @@ def test_sandwich_refusals(kw, status):
     assert B.h3blk_sandwich_norm(_sandwich(**kw), None) == status
 
 
+def test_packed_sandwich_is_the_structure():
+    from joint_video_audio_b200 import fp4 as F
+    v = (7, 256, 4, 2, 1, 1, 1e-5, 2e-5, 0.5, *(p(k) for k in range(1, 11)), 1)
+    raw = F._pack_sandwich(*v)
+    s = B.h3blk_sandwich.from_buffer_copy(raw)
+    got = [getattr(s, n) for n, _ in B.h3blk_sandwich._fields_]
+    got[-2] = C.cast(s.h_fp4, C.c_void_p).value
+    assert len(raw) == C.sizeof(B.h3blk_sandwich) and got[:6] == list(v[:6]) and got[9:] == list(v[9:])
+    assert [round(f, 9) for f in got[6:9]] == [round(f, 9) for f in v[6:9]]
+
+
 def test_null_structs():
     assert B._lib.h3blk_sandwich_norm(None, None) == BAD
     assert B._lib.h3blk_gemm_fp4(None, None, 0, 0, p(1), 128, None) == BAD
