@@ -46,12 +46,14 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int blk = threadIdx.x >> 2, l = threadIdx.x & 3, g = lane >> 2;
   const uint32_t row_bytes = (uint32_t)K * 2u;
+  pdl_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
     fail[0] = fail[1] = 0;
     fence_mbar_init();
   }
   __syncthreads();
+  pdl_wait();
   auto issue = [&](int64_t row, int slot) {
     if (row >= rows) return;
     mbar_expect_tx(&full[slot], row_bytes);
@@ -204,6 +206,8 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
   const int lane = threadIdx.x & 31;
   const int64_t gw = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int64_t row = gw / warps;
+  pdl_launch();
+  pdl_wait();
   if (row >= rows) return;
   const int blk = (int)(gw - row * warps) * 8 + (lane >> 2), l = lane & 3;
   uint4 c = make_uint4(0, 0, 0, 0);
@@ -262,11 +266,11 @@ cudaError_t launch_quant_t(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
   if (smem > 40 * 1024 &&
       (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
     return e;
-  const int64_t most = (int64_t)num_sms * resident_ctas(threads, 64, smem);
+  const int64_t most = (int64_t)num_sms * resident_ctas<quantize_fp4_kernel<FMT, ROT>>(threads, smem);
   const int64_t grid = a.rows < most ? a.rows : most;
-  kern<<<(unsigned)grid, threads, smem, s>>>(a.in, a.ld, a.rows, a.K, fp4_katoms(FMT, a.K), stages, a.codes, a.scales,
-                                             a.row_scale);
-  return cudaGetLastError();
+  ChainedLaunch l(dim3((unsigned)grid), threads, smem, s);
+  return cudaLaunchKernelEx(&l.cfg, kern, a.in, a.ld, a.rows, a.K, fp4_katoms(FMT, a.K), stages, a.codes, a.scales,
+                            a.row_scale);
 }
 
 template <int FMT, typename T>
@@ -274,9 +278,9 @@ cudaError_t launch_dequant_t(const Fp4DequantArgs& a, cudaStream_t s) {
   const int warps = (a.K + 1023) / 1024;
   const int64_t grid = (a.rows * warps + 7) / 8;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  dequantize_fp4_kernel<FMT, T><<<(unsigned)grid, 256, 0, s>>>(a.codes, a.scales, a.row_scale, a.rows, a.K,
-                                                               fp4_katoms(FMT, a.K), warps, static_cast<T*>(a.out), a.ld);
-  return cudaGetLastError();
+  ChainedLaunch l(dim3((unsigned)grid), 256, 0, s);
+  return cudaLaunchKernelEx(&l.cfg, dequantize_fp4_kernel<FMT, T>, a.codes, a.scales, a.row_scale, a.rows, a.K,
+                            fp4_katoms(FMT, a.K), warps, static_cast<T*>(a.out), a.ld);
 }
 
 }  // namespace

@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(kFewThreads)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   volatile int* vabort = abort;
+  pdl_launch();  // (behind the allocation: a later kernel's CTA may wait for these columns, but cannot hold them)
+  pdl_wait();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -555,6 +557,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   // all 512 columns are this CTA's, so they start at address 0: a constant
   // that the issue loop need not carry (checked all the same)
   if (*tmem_slot != 0) *abort = 1;
+  pdl_launch();  // (behind the allocation: a later kernel's CTA may wait for these columns, but cannot hold them)
+  pdl_wait();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer (both CTAs)
@@ -799,19 +803,9 @@ cudaError_t launch_few_t(const Fp4GemmArgs& p, const Maps& m, int num_sms, cudaS
   const int stages = (p.K + kBlockK - 1) / kBlockK;
   int split = 1;
   while (split < 8 && tiles * split * 2 <= (int64_t)Cfg::kPerSm * num_sms && stages >= 2 * split * kMinStages) split *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.N + 127) / 128, (unsigned)((p.M + NT - 1) / NT), split);
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = split;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, m.b, m.a, m.bs, m.as, p);
+  ChainedLaunch l(dim3((p.N + 127) / 128, (unsigned)((p.M + NT - 1) / NT), split), kFewThreads, Cfg::kSmem, s,
+                  dim3(1, 1, split));
+  return cudaLaunchKernelEx(&l.cfg, k, m.b, m.a, m.bs, m.as, p);
 }
 
 template <int FMT, int NT>
@@ -830,19 +824,8 @@ cudaError_t launch_pair_t(const Fp4GemmArgs& p, const Maps& m, int num_sms, cuda
   const int64_t tiles = (p.M + 255) / 256 * (SWIGLU ? p.N / 128 : ((int64_t)p.N + 255) / 256);
   if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
   const int clusters = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, m.a, m.b, m.as, m.bs, m.out, p);
+  ChainedLaunch l(dim3(2 * clusters), kPairThreads, Cfg::kSmem, s, dim3(2));
+  return cudaLaunchKernelEx(&l.cfg, k, m.a, m.b, m.as, m.bs, m.out, p);
 }
 
 // Rows up to which the few-rows kernel runs: above them the pair kernel. Both

@@ -187,14 +187,51 @@ struct SandwichArgs {
   float* row_scale;
 };
 cudaError_t launch_sandwich(const SandwichArgs& a, int num_sms, cudaStream_t s);
-// CTAs of a persistent row pass that an SM holds, by threads, registers per
-// thread and shared memory (an estimate: more or fewer only shift the balance).
-inline int resident_ctas(int threads, int regs, size_t smem) {
-  const int by_threads = 2048 / threads, by_regs = 65536 / (threads * regs), by_smem = (int)(224 * 1024 / (smem + 4096));
+// CTAs of a kernel that an SM holds at once. The persistent row passes launch
+// exactly that many per SM: with fewer, the SMs that a preceding kernel leaves
+// first would fill up and take the work of those it leaves last.
+template <auto kKernel>
+int resident_ctas(int threads, size_t smem) {
+  static const cudaFuncAttributes f = [] {
+    cudaFuncAttributes a{};
+    if (cudaFuncGetAttributes(&a, kKernel) != cudaSuccess) a.numRegs = 128;
+    return a;
+  }();
+  const int warps = (threads + 31) / 32;
+  const int by_threads = 64 / warps;
+  // a quarter of the SM has 16,384 registers and gives them out to warps, eight a thread at a time
+  const int by_regs = 16384 / (32 * ((f.numRegs + 7) & ~7)) * 4 / warps;
+  const int by_smem = (int)((228 * 1024) / (smem + f.sharedSizeBytes + 1024));  // 1 KB of a CTA's is the system's
   int n = by_threads < by_regs ? by_threads : by_regs;
   n = by_smem < n ? by_smem : n;
   return n < 1 ? 1 : n > 32 ? 32 : n;
 }
+
+// A launch whose CTAs may start while the kernel before it in the stream ends:
+// the kernel sets itself up, then waits (pdl_wait) for that kernel's end before
+// it touches memory. Behind a kernel that does not call pdl_launch, or anything
+// but a kernel, it starts at that one's end as any other.
+struct ChainedLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  ChainedLaunch(dim3 grid, int threads, size_t smem, cudaStream_t s, dim3 cluster = dim3(0)) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cluster.x) {
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim.x = cluster.x;
+      attr[1].val.clusterDim.y = cluster.y;
+      attr[1].val.clusterDim.z = cluster.z;
+      cfg.numAttrs = 2;
+    }
+  }
+};
 
 // ---------------------------------------------------------------- attention
 struct AttnArgs {

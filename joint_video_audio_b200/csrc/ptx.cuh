@@ -164,6 +164,12 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// Waits until the kernel before this one in the stream has ended and its writes
+// are visible (at once for a kernel launched without that overlap); lets the
+// kernel after it start its set-up once every CTA here has started.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // The same without release semantics, for an arrival that hands over tensor
 // memory whose reads have completed (tcgen05.wait::ld) and nothing else. The
 // release form also waits for the thread's outstanding global accesses:

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
   const int64_t per = (a.rows + gridDim.x - 1) / gridDim.x;
   const int64_t s0 = (int64_t)blockIdx.x * per;
   const int64_t s1 = s0 + per < a.rows ? s0 + per : a.rows;
+  pdl_launch();
   if (s0 >= s1) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
     fence_mbar_init();
   }
   for (int i = threadIdx.x; i < 2 * 3 * R * 32; i += blockDim.x) (&red[0][0][0][0])[i] = 0.f;
+  pdl_wait();
   const float inv_c = 1.f / (float)a.C;
   Vectors vec[CPT];
   int cur = -2;  // key of the vectors held
@@ -334,10 +336,10 @@ cudaError_t launch_t(const SandwichArgs& a, int num_sms, cudaStream_t s) {
   if (smem > 40 * 1024 &&
       (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
     return e;
-  const int64_t most = (int64_t)num_sms * resident_ctas(threads, MAXT == 1024 ? 64 : 88, smem);
+  const int64_t most = (int64_t)num_sms * resident_ctas<sandwich_kernel<HOUT, ROT, CPT, MAXT, R>>(threads, smem);
   const int64_t grid = a.rows < most ? a.rows : most;
-  kern<<<(unsigned)grid, threads, smem, s>>>(a, stages, HOUT >= 2 ? fp4_katoms(HOUT == 3 ? kFp4NV : kFp4MX, a.C) : 0);
-  return cudaGetLastError();
+  ChainedLaunch l(dim3((unsigned)grid), threads, smem, s);
+  return cudaLaunchKernelEx(&l.cfg, kern, a, stages, HOUT >= 2 ? fp4_katoms(HOUT == 3 ? kFp4NV : kFp4MX, a.C) : 0);
 }
 
 // Thread bounds by width, so that narrow rows leave registers for the vectors.

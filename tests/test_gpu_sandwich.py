@@ -212,3 +212,51 @@ def test_offsets_past_32_bits(j, h):
     else:
         assert torch.equal(hl.codes.view(reps, -1), h1.codes.view(1, -1).expand(reps, -1))
         assert torch.equal(hl.row_scale.view(reps, -1), h1.row_scale.expand(reps, -1))
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("n", [1, 40, 600, 3000])
+def test_back_to_back_calls_in_the_same_buffers(j, n, graph):
+    """A kernel starts its set-up while the one before it ends. Calls in a row
+    that write what the one before reads and read what it writes, with a torch
+    kernel or a copy between them at times, give the bits of the same calls one
+    at a time."""
+    c, f = 512, 1024
+    d = {k: v.cuda() for k, v in _case(n, c, 41).items()}
+    g = torch.Generator().manual_seed(42)
+    up = j.quantize_fp4((torch.randn(f, c, generator=g) / 23).to(torch.bfloat16).cuda(), "nv")
+    down = j.quantize_fp4((torch.randn(c, f, generator=g) / 32).to(torch.bfloat16).cuda(), "nv")
+
+    def run(wait):
+        x, y = d["x"].clone(), d["y"].clone()
+        a, h = torch.empty(n, f, dtype=torch.bfloat16, device="cuda"), torch.empty_like(x)
+        qh, qa = j.Fp4Tensor(n, c, "nv"), j.Fp4Tensor(n, f, "nv")
+        seen = []
+        for i in range(6):
+            for step in (lambda: h.copy_(j.sandwich_norm(x, y, d["tag"], d["tidx"], d["table"], branch_scale=0.5, x_out=x)[1]),
+                         lambda: j.quantize_fp4(h, "nv", out=qh),
+                         lambda: j.gemm_fp4(qh, up, out=a),
+                         lambda: j.quantize_fp4(a, "nv", out=qa),
+                         lambda: j.gemm_fp4(qa, down, out=y),
+                         lambda: a.zero_() if i % 2 else j.dequantize_fp4(qa, out=a),
+                         lambda: j.quantize_fp4(y, "nv", out=qh),
+                         lambda: j.dequantize_fp4(qh, out=y)):
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+            seen.append((x + 0, y + 0, a + 0))
+        return seen
+
+    ref = run(True)
+    if graph:
+        run(False)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = run(False)
+        for _ in range(3):
+            g.replay()
+    else:
+        got = [run(False) for _ in range(3)][-1]
+    torch.cuda.synchronize()
+    for r, s in zip(ref, got):
+        assert all(torch.equal(u, v) for u, v in zip(r, s))
