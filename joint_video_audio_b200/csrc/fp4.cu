@@ -13,6 +13,7 @@ namespace h3 {
 namespace {
 
 constexpr int kMaxRowWarps = 16;  // 1024 channels each: K <= 16384
+constexpr int kGroupWarps = 4;    // of a group of narrow rows
 constexpr int kMaxStages = 4;
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -21,31 +22,46 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Persistent CTAs of as many warps as a row of 1024 channels each takes, one
-// row at a time (row = blockIdx.x + i * gridDim.x), four lanes to a block of
-// 128 channels. Rows arrive by bulk copies issued `stages` rows ahead. NV needs
-// the row's largest magnitude before its first code: the barrier that hands a
-// slot back for refilling is also that reduction's.
+__device__ __forceinline__ float warp_max(float v) {  // of values that are not negative
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
+// Persistent CTAs, R rows at a time (rows grp R .. of grp = blockIdx.x + i *
+// gridDim.x), four lanes to a block of 128 channels. Rows arrive by bulk copies
+// issued `stages` groups ahead. R is 1 and a CTA as many warps as a row of 1024
+// channels each takes, or, GROUPED, rows of up to 512 channels share 4 warps,
+// `pitch` blocks (2 or 4) to a row. NV needs the row's largest magnitude before
+// its first code: the barrier that hands a slot back for refilling is also that
+// reduction's; narrow rows lie inside a warp.
 //
 // Measured (32768 x 14336, 2.53 / 2.56 bytes a value): MX 205 us (5.8 TB/s, 89 %
 // of the copy rate), MX rotated 209 us, NV 219 us, NV rotated 285 us, the last
 // two bound by issue (2.6-2.7 instructions a cycle). One row per CTA at a time
-// without the ring took 240, 338, 379 and 467 us.
+// without the ring took 240, 338, 379 and 467 us. Grouped (131072 x 256): MX 22
+// us, NV 27 us, one row at a time 47 and 64; groups of two rows of 5376: MX 86 us
+// as without, NV 127 instead of 98.
 //
-// A lane works on 32 channels: unrotated the 32 from 32 threadIdx.x (an MX
+// A lane works on 32 channels: unrotated the l-th 32 of its block (an MX
 // block, two NV blocks; its 16-byte reads of the row in an order that gives
 // each eight lanes distinct banks), rotated as fwht128_warp leaves them.
-template <int FMT, bool ROT>
-__global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
+template <int FMT, bool ROT, bool GROUPED>
+__global__ void __launch_bounds__(GROUPED ? kGroupWarps * 32 : kMaxRowWarps * 32, GROUPED ? 7 : 2)
     quantize_fp4_kernel(const __nv_bfloat16* __restrict__ in, int64_t ld, int64_t rows, int K, int katoms, int stages,
-                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, float* __restrict__ row_scale) {
+                        int pitch, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, float* __restrict__ row_scale) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kMaxStages];
   __shared__ float red[2][kMaxRowWarps];
   __shared__ int fail[2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int blk = threadIdx.x >> 2, l = threadIdx.x & 3, g = lane >> 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = threadIdx.x & 3, g = lane >> 2;
+  const int R = GROUPED ? kGroupWarps * 8 / pitch : 1;
   const uint32_t row_bytes = (uint32_t)K * 2u;
+  const int64_t groups = GROUPED ? (rows + R - 1) / R : rows;
+  // row of the group and block of the row: as the lane loads them, and, rotated,
+  // of the values it then holds (those of block b and the next)
+  const int f_in = threadIdx.x >> 2, f = ROT ? warp * 8 + 2 * l : f_in;
+  const int r_in = GROUPED ? f_in / pitch : 0, blk = GROUPED ? f_in % pitch : f_in;
+  const int r = GROUPED ? f / pitch : 0, b = GROUPED ? f % pitch : f;
   pdl_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
@@ -54,26 +70,34 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
   }
   __syncthreads();
   pdl_wait();
-  auto issue = [&](int64_t row, int slot) {
-    if (row >= rows) return;
-    mbar_expect_tx(&full[slot], row_bytes);
-    bulk_load(ring + (uint32_t)slot * row_bytes, in + row * ld, row_bytes, &full[slot]);
+  auto rows_of = [&](int64_t grp) { return !GROUPED || rows - grp * R > R ? R : (int)(rows - grp * R); };
+  auto issue = [&](int64_t grp, int slot) {
+    if (grp >= groups) return;
+    const int n = rows_of(grp);
+    uint8_t* dst = ring + (uint32_t)(slot * R) * row_bytes;
+    const __nv_bfloat16* src = in + grp * R * ld;
+    mbar_expect_tx(&full[slot], n * row_bytes);
+    if (!GROUPED || ld == K)
+      bulk_load(dst, src, n * row_bytes, &full[slot]);
+    else
+      for (int i = 0; i < n; ++i) bulk_load(dst + i * row_bytes, src + i * ld, row_bytes, &full[slot]);
   };
   if (threadIdx.x == 0)
     for (int i = 0; i < stages; ++i) issue(blockIdx.x + (int64_t)i * gridDim.x, i);
   int st = 0, phase = 0, par = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
+  for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x, par ^= 1) {
     if (!mbar_wait(&full[st], phase, nullptr)) fail[par] = 1;
+    const int n = rows_of(grp);
     // the lane's chunks: slot w holds chunk w ^ perm of its 32 channels;
     // rotated, odd blocks take theirs in swapped pairs
-    const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)st * row_bytes);
+    const uint4* src = reinterpret_cast<const uint4*>(ring + (uint32_t)(st * R + r_in) * row_bytes);
     const int perm = ROT ? blk & 1 : (threadIdx.x >> 1) & 3;
     uint4 v[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const int c = ROT ? blk * 16 + (w >> 1) * 8 + 2 * l + ((w & 1) ^ perm) : threadIdx.x * 4 + (w ^ perm);
+      const int c = ROT ? blk * 16 + (w >> 1) * 8 + 2 * l + ((w & 1) ^ perm) : blk * 16 + l * 4 + (w ^ perm);
       v[w] = make_uint4(0, 0, 0, 0);
-      if (c * 8 < K) v[w] = src[c];
+      if ((!GROUPED || r_in < n) && c * 8 < K) v[w] = src[c];
     }
     // the largest magnitudes of its two groups of 16 channels; of the MX block
     // that each belongs to
@@ -92,33 +116,39 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
     } else {
       if (finite_bits(am[0])) top = am[0];
       if (finite_bits(am[1])) top = fmaxf(top, am[1]);
-    }
-    if (FMT == kFp4NV) {
-      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-      if (lane == 0) red[par][warp] = top;
+      if (GROUPED) {  // over the lanes of the row: rotated, all g and the l of its pairs of blocks
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1)
+          if (ROT ? m >= 4 || 2 * m < pitch : m < 4 * pitch) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      } else {
+        top = warp_max(top);
+        if (lane == 0) red[par][warp] = top;
+      }
     }
     __syncthreads();  // every thread has read the slot
     if (fail[par]) {  // a load never landed: those in flight must before the CTA's shared memory goes
       if (threadIdx.x == 0)
-        for (int i = 0; i < stages && row + (int64_t)i * gridDim.x < rows; ++i) {
+        for (int i = 0; i < stages && grp + (int64_t)i * gridDim.x < groups; ++i) {
           mbar_wait(&full[st], phase, nullptr);
           if (++st == stages) st = 0, phase ^= 1;
         }
       return;
     }
     if (threadIdx.x == 0) {
-      fail[par ^ 1] = 0;  // every thread passed the last row's check of that flag
+      fail[par ^ 1] = 0;  // every thread passed the last group's check of that flag
       fence_proxy_async_smem();
-      issue(row + (int64_t)stages * gridDim.x, st);
+      issue(grp + (int64_t)stages * gridDim.x, st);
     }
     if (++st == stages) st = 0, phase ^= 1;
     int e_row = 0;
     if (FMT == kFp4NV) {
-      top = lane < warps ? red[par][lane] : 0.f;
-      e_row = nv_row_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+      if (!GROUPED) top = warp_max(lane < (int)(blockDim.x >> 5) ? red[par][lane] : 0.f);
+      e_row = nv_row_exponent(top);
     }
+    const int64_t row = grp * R + r;
+    const bool live = !GROUPED || r < n;
     constexpr float kRot = 0.08838834764831845f;  // 1 / sqrt(128)
-    if (threadIdx.x == 0) row_scale[row] = pow2_float(e_row) * (ROT ? kRot : 1.f);
+    if (GROUPED ? live && b == 0 && (ROT ? g : l) == 0 : threadIdx.x == 0) row_scale[row] = pow2_float(e_row) * (ROT ? kRot : 1.f);
     uint32_t q[4], sc[2];
     const int lift = e_row < kNvSmall ? kNvLift : 0;
     float inv = 0.f;
@@ -136,9 +166,8 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
     uint8_t* crow = codes + row * (K >> 1);
     if (ROT) {
       // K is a multiple of 128: blocks are whole. 16 channels each of blocks b, b + 1
-      const int b = warp * 8 + 2 * l;
-      if (b * 128 < K) *reinterpret_cast<uint2*>(crow + b * 64 + g * 8) = make_uint2(q[0], q[1]);
-      if (b * 128 + 128 < K) *reinterpret_cast<uint2*>(crow + b * 64 + 64 + g * 8) = make_uint2(q[2], q[3]);
+      if (live && b * 128 < K) *reinterpret_cast<uint2*>(crow + b * 64 + g * 8) = make_uint2(q[0], q[1]);
+      if (live && b * 128 + 128 < K) *reinterpret_cast<uint2*>(crow + b * 64 + 64 + g * 8) = make_uint2(q[2], q[3]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (FMT == kFp4MX) {  // byte g / 2 of the block's word
@@ -152,21 +181,20 @@ __global__ void __launch_bounds__(kMaxRowWarps * 32, 2)
         }
       }
       const int i = g & 1;  // lanes g = 0, 1 store block b's, b + 1's (first) word, for NV g = 4, 5 the second
-      if ((g & 2) == 0 && (FMT == kFp4NV || g < 4) && (b + i) * 128 < K)
+      if ((g & 2) == 0 && (FMT == kFp4NV || g < 4) && live && (b + i) * 128 < K)
         *fp4_scale_word(scales, row, katoms, FMT == kFp4MX ? b + i : 2 * (b + i) + (g >> 2)) = i ? sc[1] : sc[0];
     } else {
       // the words back in the channels' order
       const bool s1 = perm & 1, s2 = perm & 2;
       const uint32_t a0 = s1 ? q[1] : q[0], a1 = s1 ? q[0] : q[1], a2 = s1 ? q[3] : q[2], a3 = s1 ? q[2] : q[3];
-      const bool ok = threadIdx.x * 32 < K;
+      const bool ok = live && blk * 128 + l * 32 < K;
       if (ok)
-        *reinterpret_cast<uint4*>(crow + threadIdx.x * 16) =
-            s2 ? make_uint4(a2, a3, a0, a1) : make_uint4(a0, a1, a2, a3);
+        *reinterpret_cast<uint4*>(crow + blk * 64 + l * 16) = s2 ? make_uint4(a2, a3, a0, a1) : make_uint4(a0, a1, a2, a3);
       if (FMT == kFp4MX) {
         uint32_t s = (ok ? sc[0] : 1u) << (8 * l);  // (past K: the smallest scale)
         s |= __shfl_xor_sync(0xffffffffu, s, 1);
         s |= __shfl_xor_sync(0xffffffffu, s, 2);
-        if (l == 0 && blk * 128 < K) *fp4_scale_word(scales, row, katoms, blk) = s;
+        if (l == 0 && ok) *fp4_scale_word(scales, row, katoms, blk) = s;
       } else {
         uint32_t s = (s2 ? sc[1] | sc[0] << 8 : sc[0] | sc[1] << 8) << (16 * (l & 1));
         s |= __shfl_xor_sync(0xffffffffu, s, 1);
@@ -255,22 +283,28 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
   }
 }
 
-template <int FMT, bool ROT>
+template <int FMT, bool ROT, bool GROUPED>
 cudaError_t launch_quant_t(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
-  auto kern = quantize_fp4_kernel<FMT, ROT>;
-  const int threads = 32 * ((a.K + 1023) / 1024);
+  constexpr auto kern = quantize_fp4_kernel<FMT, ROT, GROUPED>;
+  const int pitch = a.K <= 256 ? 2 : 4, R = GROUPED ? kGroupWarps * 8 / pitch : 1;
+  const int threads = 32 * (GROUPED ? kGroupWarps : (a.K + 1023) / 1024);
   if (threads > 32 * kMaxRowWarps) return cudaErrorInvalidValue;
   const int stages = a.K <= 2048 ? kMaxStages : 3;
-  const size_t smem = (size_t)stages * a.K * 2;
+  const size_t smem = (size_t)stages * R * a.K * 2;
   cudaError_t e;
   if (smem > 40 * 1024 &&
       (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
     return e;
-  const int64_t most = (int64_t)num_sms * resident_ctas<quantize_fp4_kernel<FMT, ROT>>(threads, smem);
-  const int64_t grid = a.rows < most ? a.rows : most;
+  const int64_t most = (int64_t)num_sms * resident_ctas<kern>(threads, smem);
+  const int64_t groups = (a.rows + R - 1) / R, grid = groups < most ? groups : most;
   ChainedLaunch l(dim3((unsigned)grid), threads, smem, s);
-  return cudaLaunchKernelEx(&l.cfg, kern, a.in, a.ld, a.rows, a.K, fp4_katoms(FMT, a.K), stages, a.codes, a.scales,
+  return cudaLaunchKernelEx(&l.cfg, kern, a.in, a.ld, a.rows, a.K, fp4_katoms(FMT, a.K), stages, pitch, a.codes, a.scales,
                             a.row_scale);
+}
+
+template <int FMT, bool ROT>
+cudaError_t launch_quant(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
+  return a.K <= 512 ? launch_quant_t<FMT, ROT, true>(a, num_sms, s) : launch_quant_t<FMT, ROT, false>(a, num_sms, s);
 }
 
 template <int FMT, typename T>
@@ -287,8 +321,8 @@ cudaError_t launch_dequant_t(const Fp4DequantArgs& a, cudaStream_t s) {
 
 cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
   if (a.rows <= 0) return cudaSuccess;
-  if (a.nv) return a.rotate ? launch_quant_t<kFp4NV, true>(a, num_sms, s) : launch_quant_t<kFp4NV, false>(a, num_sms, s);
-  return a.rotate ? launch_quant_t<kFp4MX, true>(a, num_sms, s) : launch_quant_t<kFp4MX, false>(a, num_sms, s);
+  if (a.nv) return a.rotate ? launch_quant<kFp4NV, true>(a, num_sms, s) : launch_quant<kFp4NV, false>(a, num_sms, s);
+  return a.rotate ? launch_quant<kFp4MX, true>(a, num_sms, s) : launch_quant<kFp4MX, false>(a, num_sms, s);
 }
 
 cudaError_t launch_dequantize_fp4(const Fp4DequantArgs& a, cudaStream_t s) {

@@ -304,3 +304,29 @@ def test_offsets_past_32_bits(j, fmt):
     w = j.quantize_fp4((torch.randn(n, k, generator=g) / 128).to(torch.bfloat16).cuda(), fmt)
     y, first = j.gemm_fp4(q, w), j.gemm_fp4(one, w)
     assert torch.equal(y.view(reps, -1), first.view(1, -1).expand(reps, -1))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("rotate", [False, True])
+@pytest.mark.parametrize("rows,k,stride", [(1, 128, 128), (15, 256, 256), (17, 256, 296), (16, 384, 384), (9, 384, 400),
+                                           (7, 512, 512), (70003, 128, 136), (20001, 512, 512), (5, 640, 640),
+                                           (33, 32, 40), (18, 288, 288), (30000, 480, 488)])
+def test_narrow_rows(j, fmt, rotate, rows, k, stride):
+    """Several rows to a warp: integers, whose rotated sums are exact; a row's
+    scale is its own, and non-finite values stay in their block."""
+    if rotate and k % 128:
+        pytest.skip("a rotation takes whole blocks of 128")
+    g = torch.Generator().manual_seed(rows + k)
+    wide = torch.randint(-128, 129, (rows, stride), generator=g).to(torch.bfloat16)
+    wide *= torch.exp2(torch.randint(-30, 31, (rows, 1), generator=g)).to(torch.bfloat16)
+    x = wide[:, :k]
+    if rows > 4:
+        x[rows // 2] = 0
+        if not rotate:
+            x[1, 3], x[rows - 1, k - 1] = float("inf"), float("nan")
+    q = j.Fp4Tensor(rows, k, fmt)
+    q.buffer.fill_(0xEE)
+    j.quantize_fp4(wide.cuda()[:, :k], fmt, rotate=rotate, out=q)
+    assert_same_bits(q, o.quantize(x, fmt, rotate))
+    pads = q.scales.cpu().numpy().reshape(-1)[o.scale_offsets(-(-rows // 128) * 128, k // o.BLOCK[fmt])[rows:]]
+    assert np.all(pads == 0xEE)
