@@ -225,25 +225,40 @@ __device__ __forceinline__ uint4 group_transpose(const uint32_t (&w)[4], int lan
 }
 
 // 32 channels a lane, read as one 16-byte piece of codes and transposed among
-// four lanes so that the values leave in 64-byte runs. Measured (32768 x 14336
-// -> bf16): 186 us MX, 192 us NV, 97 and 95 % of the copy rate.
+// four lanes so that the values leave in 64-byte runs. Measured (32768 x 14336):
+// to bf16 186 us MX, 190 us NV, 97 and 96 % of the copy rate, to fp32 322 us (404
+// with a lane's eight values in one run). Blocks of all rows are numbered
+// through: a warp per 1024 channels of a row took 82 us for 32768 x 5376, not 76,
+// and 47 us for 131072 x 256, not 21.
 template <int FMT, typename T>
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __restrict__ codes, uint8_t* scales,
                                                            const float* __restrict__ row_scale, int64_t rows, int K,
-                                                           int katoms, int warps, T* __restrict__ out, int64_t ld) {
+                                                           int katoms, int blocks, T* __restrict__ out, int64_t ld) {
   const int lane = threadIdx.x & 31;
-  const int64_t gw = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int64_t row = gw / warps;
+  // four lanes to a block of 128 channels
+  const int64_t gb = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 2;
+  const int64_t row = gb / blocks;
   pdl_launch();
   pdl_wait();
-  if (row >= rows) return;
-  const int blk = (int)(gw - row * warps) * 8 + (lane >> 2), l = lane & 3;
+  const int blk = (int)(gb - row * blocks), l = lane & 3;
   uint4 c = make_uint4(0, 0, 0, 0);
-  if (blk * 128 + l * 32 < K) c = __ldg(reinterpret_cast<const uint4*>(codes + row * (K >> 1) + blk * 64 + l * 16));
+  if (row < rows && blk * 128 + l * 32 < K)
+    c = __ldg(reinterpret_cast<const uint4*>(codes + row * (K >> 1) + blk * 64 + l * 16));
   const uint32_t in[4] = {c.x, c.y, c.z, c.w};
   const uint4 t = group_transpose(in, lane);
-  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-  if (blk * 128 >= K) return;
+  uint32_t w[4] = {t.x, t.y, t.z, t.w};
+  // The lane's 32 values are four runs of eight, of channels 32 j + 8 l ..; in
+  // fp32 eight half runs, of 32 j + 4 l .. and 16 behind, so that four lanes'
+  // 16-byte stores lie side by side.
+  if (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int from = (lane & 28) + (l >> 1);
+      const uint32_t a = __shfl_sync(0xffffffffu, w[j], from), b = __shfl_sync(0xffffffffu, w[j], from + 2);
+      w[j] = __byte_perm(a, b, (l & 1) ? 0x7632 : 0x5410);
+    }
+  }
+  if (row >= rows) return;
   uint32_t s0, s1 = 0;
   if (FMT == kFp4MX) {
     s0 = *fp4_scale_word(scales, row, katoms, blk);
@@ -254,31 +269,27 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
   const float rs = __ldg(row_scale + row);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int ch = blk * 128 + j * 32 + l * 8;
-    if (ch >= K) break;
-    // MX: block j; NV: block 2 j + l / 2 of the 128 channels
-    float s;
+    if (blk * 128 + j * 32 >= K) break;  // (K is a multiple of 32)
+    // MX: block j; NV: blocks 2 j and 2 j + 1 of the 128 channels
+    float sc[2];
     if (FMT == kFp4MX) {
-      s = e8m0_value((s0 >> (8 * j)) & 0xffu);
+      sc[0] = sc[1] = e8m0_value((s0 >> (8 * j)) & 0xffu);
     } else {
-      const uint32_t word = j < 2 ? s0 : s1;
-      s = e4m3_value((word >> (16 * (j & 1) + 8 * (l >> 1))) & 0xffu);
+      const uint32_t pair = (j < 2 ? s0 : s1) >> (16 * (j & 1));
+      sc[0] = e4m3_value((pair >> (sizeof(T) == 2 ? 8 * (l >> 1) : 0)) & 0xffu);
+      sc[1] = sizeof(T) == 2 ? sc[0] : e4m3_value((pair >> 8) & 0xffu);
     }
     float v[8];
     e2m1x8_values(w[j], v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = v[e] * s * rs;  // code times block scale is exact
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * sc[e >> 2] * rs;  // code times block scale is exact
+    T* o = out + row * ld + blk * 128 + j * 32;
     if (sizeof(T) == 2) {
-      uint4 o;
-      o.x = pack_bf16x2(v[0], v[1]);
-      o.y = pack_bf16x2(v[2], v[3]);
-      o.z = pack_bf16x2(v[4], v[5]);
-      o.w = pack_bf16x2(v[6], v[7]);
-      *reinterpret_cast<uint4*>(out + row * ld + ch) = o;
+      *reinterpret_cast<uint4*>(o + l * 8) =
+          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     } else {
-      float4* d = reinterpret_cast<float4*>(out + row * ld + ch);
-      d[0] = make_float4(v[0], v[1], v[2], v[3]);
-      d[1] = make_float4(v[4], v[5], v[6], v[7]);
+      *reinterpret_cast<float4*>(o + l * 4) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(o + 16 + l * 4) = make_float4(v[4], v[5], v[6], v[7]);
     }
   }
 }
@@ -309,12 +320,12 @@ cudaError_t launch_quant(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
 
 template <int FMT, typename T>
 cudaError_t launch_dequant_t(const Fp4DequantArgs& a, cudaStream_t s) {
-  const int warps = (a.K + 1023) / 1024;
-  const int64_t grid = (a.rows * warps + 7) / 8;
+  const int blocks = (a.K + 127) / 128;
+  const int64_t grid = (a.rows * blocks + 63) / 64;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   ChainedLaunch l(dim3((unsigned)grid), 256, 0, s);
   return cudaLaunchKernelEx(&l.cfg, dequantize_fp4_kernel<FMT, T>, a.codes, a.scales, a.row_scale, a.rows, a.K,
-                            fp4_katoms(FMT, a.K), warps, static_cast<T*>(a.out), a.ld);
+                            fp4_katoms(FMT, a.K), blocks, static_cast<T*>(a.out), a.ld);
 }
 
 }  // namespace
