@@ -260,3 +260,51 @@ def test_back_to_back_calls_in_the_same_buffers(j, n, graph):
     torch.cuda.synchronize()
     for r, s in zip(ref, got):
         assert all(torch.equal(u, v) for u, v in zip(r, s))
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("n", [20, 2000])
+def test_streams_that_wait_for_one_another(j, n, graph):
+    """One stream makes inputs slowly, another one works on them behind an
+    event, and the first overwrites them behind an event of the second: a
+    kernel that starts early still waits for the events before it."""
+    c, steps = 512, 5
+    g = torch.Generator().manual_seed(51)
+    xs = [torch.randn(n, c, generator=g).to(torch.bfloat16).cuda() for _ in range(steps)]
+    slow = torch.randn(2048, 2048, generator=g).cuda()
+    w = j.quantize_fp4((torch.randn(c, c, generator=g) / 23).to(torch.bfloat16).cuda(), "nv")
+    refs = [j.gemm_fp4(j.quantize_fp4(x, "nv"), w) for x in xs]
+    torch.cuda.synchronize()
+
+    def run(s1, s2):
+        buf, q = torch.zeros(n, c, dtype=torch.bfloat16, device="cuda"), j.Fp4Tensor(n, c, "nv")
+        outs = [torch.zeros(n, c, dtype=torch.bfloat16, device="cuda") for _ in xs]
+        s2.wait_stream(s1)
+        for x, y in zip(xs, outs):
+            acc = slow
+            for _ in range(4):
+                acc = acc @ slow * 0.01
+            buf.copy_(x)
+            buf += (acc[0, 0] * 0).nan_to_num().to(torch.bfloat16)  # behind the products
+            s2.wait_stream(s1)
+            with torch.cuda.stream(s2):
+                j.quantize_fp4(buf, "nv", out=q)
+            s1.wait_stream(s2)
+            buf.fill_(float("nan"))
+            with torch.cuda.stream(s2):
+                j.gemm_fp4(q, w, out=y)
+            s2.wait_stream(s1)
+        s1.wait_stream(s2)
+        return outs, buf, q
+
+    s2 = torch.cuda.Stream()
+    if graph:
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            keep = run(torch.cuda.current_stream(), s2)
+        for _ in range(3):
+            cg.replay()
+    else:
+        keep = run(torch.cuda.current_stream(), s2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(keep[0], refs))
