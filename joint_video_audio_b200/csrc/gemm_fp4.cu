@@ -797,12 +797,15 @@ cudaError_t launch_few_t(const Fp4GemmArgs& p, const Maps& m, int num_sms, cudaS
   auto k = gemm_fp4_few_kernel<FMT, NT, NW, T>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem);
   if (e != cudaSuccess) return e;
-  // K is split while the CTAs still fit on the SMs at once and each keeps
-  // kMinStages stages to stream
-  const int64_t tiles = (p.N + 127) / 128 * ((p.M + NT - 1) / NT);
+  // K is split over up to six CTAs as long as each keeps kMinStages stages to
+  // stream and their clusters fill no more than seven eighths of the SMs' places.
+  // Measured (NV, a row, us): 84 tiles x 21 stages split by 2 / 3 / 4 9.5 / 9.0 / 13.3;
+  // 56 x 21 by 3 / 4 / 5 7.0 / 7.1 / 8.1; 42 x 56 by 4 / 6 / 7 11.1 / 10.7 / 15.1.
+  const int64_t tiles = (p.N + 127) / 128 * ((p.M + NT - 1) / NT), places = (int64_t)Cfg::kPerSm * num_sms * 7 / 8;
   const int stages = (p.K + kBlockK - 1) / kBlockK;
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= (int64_t)Cfg::kPerSm * num_sms && stages >= 2 * split * kMinStages) split *= 2;
+  int split = (int)(places / tiles < 6 ? places / tiles : 6);
+  split = split > stages / kMinStages ? stages / kMinStages : split;
+  split = split < 1 ? 1 : split;
   ChainedLaunch l(dim3((p.N + 127) / 128, (unsigned)((p.M + NT - 1) / NT), split), kFewThreads, Cfg::kSmem, s,
                   dim3(1, 1, split));
   return cudaLaunchKernelEx(&l.cfg, k, m.b, m.a, m.bs, m.as, p);
