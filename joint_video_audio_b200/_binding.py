@@ -136,7 +136,7 @@ def _load():
         "h3blk_gemm_s8_s32": (i32, [i64, i32, i32, vp, vp, vp, vp]),
         "h3blk_gemm_bf16": (i32, [i64, i32, i32, vp, vp, vp, vp]),
         "h3blk_fp4_bytes": (i32, [i32, i64, i32, C.POINTER(sz), C.POINTER(sz), C.POINTER(sz)]),
-        # structs by address: C.byref(struct), an int, or the packed bytes
+        # structs by address
         "h3blk_quantize_fp4": (i32, [vp, i64, i32, vp, vp]),
         "h3blk_dequantize_fp4": (i32, [vp, i32, vp, i64, vp]),
         "h3blk_gemm_fp4": (i32, [vp, vp, i32, i32, vp, i64, vp]),

@@ -1,4 +1,5 @@
-"""Builds libh3blk.so (all CUDA sources under csrc/) in-tree for sm_100a.
+"""Builds libh3blk.so (all CUDA sources under csrc/) in-tree for sm_100a, and
+_fp4_torch.so (csrc/fp4_torch.cpp, a Python module over it for torch tensors).
 
     python joint_video_audio_b200/build.py [--force] [--verbose]
 
@@ -14,6 +15,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+from importlib.util import find_spec
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libh3blk.so")
+MODULE = os.path.join(PKG, "_fp4_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -61,8 +65,28 @@ def _compile(src, verbose):
     return obj
 
 
+def _build_module(force):
+    src = os.path.join(CSRC, "fp4_torch.cpp")
+    torch = os.path.dirname(find_spec("torch").origin)
+    version = os.path.join(torch, "version.py")  # another torch, another module
+    if not force and not _stale(MODULE, [src, version] + _headers()):
+        return
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = MODULE + ".tmp"
+    inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_path("include"), os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", src, "-o", tmp]
+    cmd += [f for d in inc for f in ("-I", d)]
+    cmd += ["-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+            "-L", PKG, "-l:libh3blk.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MODULE)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles every csrc/*.cu and links libh3blk.so; returns its path."""
+    """Compiles every csrc/*.cu, links libh3blk.so and the module over it; returns the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = _sources()
     if force:
@@ -77,6 +101,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_module(force)
     return LIB
 
 

@@ -96,17 +96,6 @@ def test_sandwich_refusals(kw, status):
     assert B.h3blk_sandwich_norm(_sandwich(**kw), None) == status
 
 
-def test_packed_sandwich_is_the_structure():
-    from joint_video_audio_b200 import fp4 as F
-    v = (7, 256, 4, 2, 1, 1, 1e-5, 2e-5, 0.5, *(p(k) for k in range(1, 11)), 1)
-    raw = F._pack_sandwich(*v)
-    s = B.h3blk_sandwich.from_buffer_copy(raw)
-    got = [getattr(s, n) for n, _ in B.h3blk_sandwich._fields_]
-    got[-2] = C.cast(s.h_fp4, C.c_void_p).value
-    assert len(raw) == C.sizeof(B.h3blk_sandwich) and got[:6] == list(v[:6]) and got[9:] == list(v[9:])
-    assert [round(f, 9) for f in got[6:9]] == [round(f, 9) for f in v[6:9]]
-
-
 def test_null_structs():
     assert B._lib.h3blk_sandwich_norm(None, None) == BAD
     assert B._lib.h3blk_gemm_fp4(None, None, 0, 0, p(1), 128, None) == BAD
@@ -138,3 +127,36 @@ def test_python_refusals():
     for kw in ({"h": "fp8"}, {"h": "bf16", "rotate": True}, {"h": None, "rotate": True}):
         with pytest.raises(ValueError):
             j.sandwich_norm(cpu, cpu, i, i, torch.zeros(4, 2, 6, 256), **kw)
+
+
+def test_python_refuses_what_is_no_tensor_or_does_not_fit():
+    with pytest.raises(TypeError, match="Tensor"):
+        j.quantize_fp4([1.0])
+    with pytest.raises(ValueError, match="fmt"):
+        j.quantize_fp4(torch.zeros(2, 32, dtype=torch.bfloat16), "fp8")
+    q = j.Fp4Tensor(4, 256, "nv", device="cpu")
+    with pytest.raises(ValueError, match="out"):
+        j.quantize_fp4(torch.zeros(4, 128, dtype=torch.bfloat16), out=q)
+    with pytest.raises(j.H3BlkError):
+        j.Fp4Tensor(4, 100, "nv", device="cpu")
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(TypeError, match="tag"):
+        j.sandwich_norm(torch.zeros(4, 256), torch.zeros(4, 256), None, i, torch.zeros(4, 2, 6, 256))
+    with pytest.raises(ValueError, match="hidden"):
+        j.sandwich_norm(torch.zeros(4, 256), torch.zeros(4, 256), i, i, torch.zeros(4, 2, 256))
+
+
+def test_refused_calls_keep_no_references():
+    import sys
+    from joint_video_audio_b200 import fp4 as F
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    q, i, t = j.Fp4Tensor(4, 256, "nv", device="cpu"), torch.zeros(4, dtype=torch.int32), torch.zeros(4, 2, 6, 256)
+    held = (x, q, q.buffer, i, t, j.H3BlkError)
+    before = [sys.getrefcount(o) for o in held]
+    for _ in range(50):
+        for call in (lambda: j.quantize_fp4(x), lambda: j.gemm_fp4(q, q), lambda: j.dequantize_fp4(q, out=x),
+                     lambda: j.sandwich_norm(x, x, i, i, t), lambda: F._host.layout(0, 4, 33), lambda: F._host.layout(0, 4),
+                     lambda: F._host.layout("mx", 4, 32)):
+            with pytest.raises((ValueError, TypeError, j.H3BlkError)):
+                call()
+    assert [sys.getrefcount(o) for o in held] == before
