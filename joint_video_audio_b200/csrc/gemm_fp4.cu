@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kFewThreads)
     }
   }
   __syncwarp();
-  if (split > 1) cluster_sync();  // no CTA leaves while another reads its sums
+  if (split > 1) cluster_sync_relaxed();  // no CTA leaves while another reads its sums
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -160,6 +160,12 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without ordering of memory: enough where threads have used what they
+// loaded of one another's shared memory and only keep it alive. The release
+// form also waits for the outputs just stored: 2300 cycles at the end of a product.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // Arrive on an mbarrier of another CTA of the cluster (cluster-window address).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
