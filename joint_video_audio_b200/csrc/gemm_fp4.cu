@@ -457,7 +457,6 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // One epilogue warp's unit: lane's row of v, as T, to the unit with the
 // 128-byte swizzle, then stored at column x, row y where that lies inside.
@@ -704,12 +703,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t acc = ((uint32_t)(quad * 32) << 16) + buf * Cfg::kAcc1 + half * 64;
       // this warp's columns of the tile's half that the other accumulator
       // overlaps (the first one's upper, the second one's lower), then the
-      // next tile's products may begin
+      // next tile's products may begin (behind the last tile nobody waits, and an
+      // arrival could come after the first CTA has left)
       uint32_t f[64];
       tmem_ld64(acc + (buf ? 0 : 128), f);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(tempty0);
+      if (lane == 0 && t + n_clusters < num_tiles) mbar_arrive_cluster_relaxed(tempty0);
       constexpr int kUnitCols = 128 / (int)sizeof(T);
       float v[64];
       if (SWIGLU) {
@@ -739,12 +739,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait();  // the output has left shared memory and reached the matrix
+    if (lane == 0) bulk_wait_read();  // the output has left shared memory (it reaches the matrix before the grid ends)
   }
   // neither CTA leaves while the other may still signal its barriers or read
-  // its memory
+  // its memory: every signal has been waited for by now, so no ordering is needed
   tc_fence_before();
-  cluster_sync();
+  cluster_sync_relaxed();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(*tmem_slot, 512);
 }

@@ -161,8 +161,9 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The same without ordering of memory: enough where threads have used what they
-// loaded of one another's shared memory and only keep it alive. The release
-// form also waits for the outputs just stored: 2300 cycles at the end of a product.
+// loaded of one another's shared memory, have nothing in flight to it, and only
+// keep it alive. The release form also waits for the outputs just stored: 2300
+// cycles at the end of a product.
 __device__ __forceinline__ void cluster_sync_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
