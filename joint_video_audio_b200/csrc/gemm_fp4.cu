@@ -6,7 +6,7 @@
 // gemm_fp4_few_kernel: products of few rows, bound by reading the weight once.
 // The weight rows take the product's M side (128 a CTA), the activations' rows
 // its N side (16 to 128), so no tensor-core row is spent on absent rows. K is
-// split over a cluster of up to eight CTAs when the weight rows alone do not
+// split over a cluster of up to six CTAs when the weight rows alone do not
 // occupy the SMs; the partial sums meet in distributed shared memory, added in
 // the order of K.
 //   warp 0      TMA producer: per stage 256 channels (128 bytes a row) of the
@@ -17,10 +17,11 @@
 // The scales' tensor-memory columns are double-buffered per stage; a buffer is
 // rewritten once the products that read it have completed.
 //
-// Measured (weights cold, launches in a row): 1 x 5376 x 7168 NV 8.3 us, 64 x
-// 21504 x 5376 NV 19 us (3.6 TB/s), 1 x 28672 x 5376 NV 17.9 us (4.9 TB/s); a launch
-// with nothing to read is 3.6 us of that. Unsplit and with an election per
-// instruction the first took 23 us.
+// Measured (weights cold, launches of a graph): 1 x 5376 x 7168 NV 7.1 us, 64 x
+// 21504 x 5376 MX 16.7 us (3.9 TB/s), 1 x 2 x 14336 x 5376 NV SwiGLU 17.2 us (5.0
+// TB/s). 4 x 256 x 768 takes 2.8 us; of the first 3.7 us are the loads (3.3 at the
+// copy rate), 1 us the sums' meeting. Unsplit and with an election per
+// instruction it took 23 us.
 //
 // gemm_fp4_pair_kernel: products of many rows, see there.
 #include <cuda_bf16.h>
@@ -51,7 +52,10 @@ struct FewCfg {
   static constexpr int kAtoms = atoms_per_stage(FMT);
   static constexpr int kScaleBytes = kAtoms * 512;
   static constexpr int kStageBytes = NW * (kTile + kScaleBytes) + NT * kRowBytes + kScaleBytes;
-  static constexpr int kStages = NT >= 64 && NW == 1 ? 3 : 4;  // two CTAs of plain products per SM
+  // up to four, as long as an SM has room for two CTAs (of SwiGLU, whose stages
+  // are twice as large, one); a fifth gained nothing at 16 rows
+  static constexpr int kFit = (228 * 1024 / (NW == 1 ? 2 : 1) - 1024 - 1280) / kStageBytes;
+  static constexpr int kStages = kFit < 4 ? kFit : 4;
   static constexpr int kAccCols = NW * NT;
   static constexpr int kSlotCols = kAtoms * (NW + 1) * 4;
   static constexpr int kCols = kAccCols + 2 * kSlotCols;
