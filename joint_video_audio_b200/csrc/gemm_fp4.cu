@@ -17,15 +17,20 @@
 // The scales' tensor-memory columns are double-buffered per stage; a buffer is
 // rewritten once the products that read it have completed.
 //
-// Measured (weights cold, launches of a graph): 1 x 5376 x 7168 NV 7.1 us, 64 x
-// 21504 x 5376 MX 16.7 us (3.9 TB/s), 1 x 2 x 14336 x 5376 NV SwiGLU 17.2 us (5.0
-// TB/s). 4 x 256 x 768 takes 2.8 us; of the first 3.7 us are the loads (3.3 at the
-// copy rate), 1 us the sums' meeting. Unsplit and with an election per
-// instruction it took 23 us.
+// Measured (weights cold, launches of a graph): 1 x 5376 x 7168 NV 6.8 us, 64 x
+// 21504 x 5376 MX 15.5 us (4.3 TB/s), 1 x 2 x 14336 x 5376 NV SwiGLU 16.8 us (5.2
+// TB/s), 128 x 21504 x 5376 MX 17.4 us. 4 x 256 x 768 takes 2.6 us; of the first 3.7
+// us are the loads (3.3 at the copy rate), 1 us the sums' meeting. Unsplit and with
+// an election per instruction it took 23 us. The last with a row's scale fetched as
+// the row is stored, one row at a time, 22 us; four at a time where K is split, and
+// the sums lie in other SMs, 128 x 5376 x 7168 took 13.6 us, not 11.5.
 //
-// gemm_fp4_pair_kernel: products of many rows, see there.
+// gemm_fp4_pair_kernel: products of many rows, see there; takes_few() chooses.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -46,6 +51,7 @@ __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g,
 
 // ------------------------------------------------------------------ few rows
 constexpr int kFewThreads = 192;
+constexpr int kMaxSplit = 6;  // CTAs that share a product's K
 
 template <int FMT, int NT, int NW>
 struct FewCfg {
@@ -271,12 +277,23 @@ __global__ void __launch_bounds__(kFewThreads)
   // activation rows, a warp a row, four weight rows a lane
   float* sums = reinterpret_cast<float*>(smem);
   bool good = false;
+  // a warp's rows of the tile: the CTA's share, every fourth of it; lane i keeps
+  // the i-th one's scale, the lane's weight rows' scales come before the products too
+  const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
+  const int first = part * 4 + warp - 2, step = 4 * split, n = n0 + 4 * lane;
+  const int count = rows > first ? (rows - first + step - 1) / step : 0;
+  float ra = 0.f;
+  float4 rb = make_float4(0.f, 0.f, 0.f, 0.f), ru = rb;
   if (warp >= 2) {
+    if (lane < count) ra = __ldg(p.a_row + m0 + first + lane * step);
+    if (n < p.N) {  // N is a multiple of 8
+      rb = __ldg(reinterpret_cast<const float4*>(p.b_row + n));
+      if (NW == 2) ru = __ldg(reinterpret_cast<const float4*>(p.b_row + p.N + n));
+    }
     good = __all_sync(0xffffffffu, mbar_wait(tfull, 0, nullptr) && !*vabort);
     tc_fence_after();
     const int quad = warp & 3;
     const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16);
-    const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
     if (good) {
 #pragma unroll 1
       for (int c = 0; c < NW * NT; c += 16) {
@@ -292,39 +309,52 @@ __global__ void __launch_bounds__(kFewThreads)
     cluster_sync();
   else
     __syncthreads();
-  const int n = n0 + 4 * lane;
-  if (good && n < p.N) {  // N is a multiple of 8
-    const float4 rb = __ldg(reinterpret_cast<const float4*>(p.b_row + n));
-    const float4 ru = NW == 2 ? __ldg(reinterpret_cast<const float4*>(p.b_row + p.N + n)) : rb;
-    const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
+  if (good) {
     const uint32_t at = smem_u32(sums) + lane * 16;
-    // the row's sums over the parts, in their order; up to eight loads in flight
+    // a row's sums over the parts, in their order
     auto add_parts = [&](int row) {
-      float4 v[8];
+      float4 v[kMaxSplit];
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
+      for (int q = 0; q < kMaxSplit; ++q)
         if (q < split) v[q] = ld_cluster_f32x4(mapa_shared(at + row * 512, q));
 #pragma unroll
-      for (int q = 1; q < 8; ++q)
+      for (int q = 1; q < kMaxSplit; ++q)
         if (q < split) v[0].x += v[q].x, v[0].y += v[q].y, v[0].z += v[q].z, v[0].w += v[q].w;
       return v[0];
     };
-    for (int c = part * 4 + warp - 2; c < rows; c += 4 * split) {
-      const int64_t m = m0 + c;
-      const float ra = __ldg(p.a_row + m);
-      const float4 g = add_parts(c);
-      float4 v = make_float4(g.x * ra * rb.x, g.y * ra * rb.y, g.z * ra * rb.z, g.w * ra * rb.w);
-      if (NW == 2) {
-        const float4 u = add_parts(NT + c);
-        v = make_float4(swiglu(v.x, u.x * ra * ru.x), swiglu(v.y, u.y * ra * ru.y), swiglu(v.z, u.z * ra * ru.z),
-                        swiglu(v.w, u.w * ra * ru.w));
+    // R rows at a time
+    auto store_rows = [&](auto at_once) {
+      constexpr int R = decltype(at_once)::value;
+#pragma unroll 1
+      for (int i = 0; i < count; i += R) {
+        float4 g[R], u[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int c = first + (i + r < count ? i + r : i) * step;
+          g[r] = add_parts(c);
+          if (NW == 2) u[r] = add_parts(NT + c);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float rar = __shfl_sync(0xffffffffu, ra, (i + r) & 31);
+          if (i + r >= count || n >= p.N) continue;
+          float4 v = make_float4(g[r].x * rar * rb.x, g[r].y * rar * rb.y, g[r].z * rar * rb.z, g[r].w * rar * rb.w);
+          if (NW == 2)
+            v = make_float4(swiglu(v.x, u[r].x * rar * ru.x), swiglu(v.y, u[r].y * rar * ru.y),
+                            swiglu(v.z, u[r].z * rar * ru.z), swiglu(v.w, u[r].w * rar * ru.w));
+          const int64_t at_out = (m0 + first + (int64_t)(i + r) * step) * p.ld + n;
+          if (sizeof(T) == 2)
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at_out) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+          else
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at_out) = v;
+        }
       }
-      if (sizeof(T) == 2)
-        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + m * p.ld + n) =
-            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-      else
-        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + m * p.ld + n) = v;
-    }
+    };
+    if (split == 1)
+      store_rows(std::integral_constant<int, NT >= 64 ? 4 : 1>{});
+    else
+      store_rows(std::integral_constant<int, 1>{});
   }
   __syncwarp();
   if (split > 1) cluster_sync_relaxed();  // no CTA leaves while another reads its sums
@@ -795,21 +825,28 @@ struct Maps {
 
 constexpr int kMinStages = 2;
 
+// CTAs that share K in the few-rows kernel: up to six, as long as each keeps
+// kMinStages stages to stream and their clusters fill no more than seven eighths
+// of the SMs' places; 0 where the unsplit tiles already take more.
+// Measured (NV, a row, us): 84 tiles x 21 stages split by 2 / 3 / 4 9.5 / 9.0 / 13.3;
+// 56 x 21 by 3 / 4 / 5 7.0 / 7.1 / 8.1; 42 x 56 by 4 / 6 / 7 11.1 / 10.7 / 15.1.
+template <int FMT, int NT, int NW>
+int few_split(const Fp4GemmArgs& p, int num_sms) {
+  const int64_t tiles = (p.N + 127) / 128 * ((p.M + NT - 1) / NT);
+  const int64_t places = (int64_t)FewCfg<FMT, NT, NW>::kPerSm * num_sms * 7 / 8;
+  const int stages = (p.K + kBlockK - 1) / kBlockK;
+  int split = (int)(places / tiles < kMaxSplit ? places / tiles : kMaxSplit);
+  if (split > stages / kMinStages) split = stages / kMinStages < 1 ? 1 : stages / kMinStages;
+  return split;
+}
+
 template <int FMT, int NT, int NW, typename T>
 cudaError_t launch_few_t(const Fp4GemmArgs& p, const Maps& m, int num_sms, cudaStream_t s) {
   using Cfg = FewCfg<FMT, NT, NW>;
   auto k = gemm_fp4_few_kernel<FMT, NT, NW, T>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem);
   if (e != cudaSuccess) return e;
-  // K is split over up to six CTAs as long as each keeps kMinStages stages to
-  // stream and their clusters fill no more than seven eighths of the SMs' places.
-  // Measured (NV, a row, us): 84 tiles x 21 stages split by 2 / 3 / 4 9.5 / 9.0 / 13.3;
-  // 56 x 21 by 3 / 4 / 5 7.0 / 7.1 / 8.1; 42 x 56 by 4 / 6 / 7 11.1 / 10.7 / 15.1.
-  const int64_t tiles = (p.N + 127) / 128 * ((p.M + NT - 1) / NT), places = (int64_t)Cfg::kPerSm * num_sms * 7 / 8;
-  const int stages = (p.K + kBlockK - 1) / kBlockK;
-  int split = (int)(places / tiles < 6 ? places / tiles : 6);
-  split = split > stages / kMinStages ? stages / kMinStages : split;
-  split = split < 1 ? 1 : split;
+  const int split = std::max(1, few_split<FMT, NT, NW>(p, num_sms));
   ChainedLaunch l(dim3((p.N + 127) / 128, (unsigned)((p.M + NT - 1) / NT), split), kFewThreads, Cfg::kSmem, s,
                   dim3(1, 1, split));
   return cudaLaunchKernelEx(&l.cfg, k, m.b, m.a, m.bs, m.as, p);
@@ -835,16 +872,30 @@ cudaError_t launch_pair_t(const Fp4GemmArgs& p, const Maps& m, int num_sms, cuda
   return cudaLaunchKernelEx(&l.cfg, k, m.a, m.b, m.as, m.bs, m.out, p);
 }
 
-// Rows up to which the few-rows kernel runs: above them the pair kernel. Both
-// measured at N, K = 5376, 7168 (NV): 128 rows 12.9 against 17.7 us, 160 rows 16.2
-// against 16.4, 512 rows 23.9 against 17.3; at N = 21504 128 rows 22.6 against
-// 23.5, 256 rows 39.5 against 25.3.
-constexpr int64_t kFewRows = 128;
+// Whether the few-rows kernel takes a product: always up to 64 rows, above them
+// where the pair kernel's tiles would leave many SMs without work or weights
+// unread. Both take a start and an end and their stages one after the other; in
+// units of a pair stage (0.4 us; SwiGLU 1.2 of them) about 11 + stages x waves,
+// and 15 + 1.6 (SwiGLU 2.2) x a CTA's stages. Measured (NV, us, few rows / pair):
+// 128 x 21504 x 5376 17.4 / 22, 128 x 2304 x 768 5.7 / 5.2, 160 x 5376 x 7168 12.2 /
+// 15.3, 160 x 7168 x 5376 13.4 / 12.8, 256 x 1024 x 7168 9.0 / 14.3, 256 x 5376 x 2048
+// 8.8 / 7.5, 384 x 10752 x 5376 16.6 / 21.7, 256 x 8192 x 14336 23.4 / 26.5; at worst the
+// rule's choice was 8 % slower (65 x 2 x 7168 x 7168 SwiGLU 16.2 / 17.6).
+template <int FMT, int NW>
+bool takes_few(const Fp4GemmArgs& p, int num_sms) {
+  if (p.M <= 64) return true;
+  const int split = few_split<FMT, 128, NW>(p, num_sms);
+  if (split == 0) return false;
+  const int64_t stages = (p.K + kBlockK - 1) / kBlockK, clusters = num_sms / 2;
+  const int64_t tiles = (p.M + 255) / 256 * ((p.N + 256 / NW - 1) / (256 / NW));
+  const int64_t few = 150 + (NW == 1 ? 16 : 22) * ((stages + split - 1) / split);
+  return few < 110 + (NW == 1 ? 10 : 12) * stages * ((tiles + clusters - 1) / clusters);
+}
 
 template <int FMT>
 cudaError_t launch_fmt(const Fp4GemmArgs& p, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms, cudaStream_t s) {
   Maps m;
-  const bool few = p.M <= kFewRows;
+  const bool few = p.swiglu ? takes_few<FMT, 2>(p, num_sms) : takes_few<FMT, 1>(p, num_sms);
   const int nt = !few ? 128 : p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   const int64_t b_rows = p.swiglu ? 2 * (int64_t)p.N : p.N;
   if (!codes_map(encode, &m.a, p.a_codes, p.M, p.K, nt) || !codes_map(encode, &m.b, p.b_codes, b_rows, p.K, 128) ||

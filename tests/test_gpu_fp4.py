@@ -384,3 +384,27 @@ def test_calls_from_two_threads(j):
     for t in threads:
         t.join(60)
     assert good == [50, 50]
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("m,n,k", [(65, 256, 256), (100, 1536, 768), (128, 512, 5376), (129, 256, 5472), (200, 512, 7168),
+                                   (385, 256, 4128), (1000, 256, 6144), (130, 1280, 14336)])
+def test_gemm_rows_between_the_kernels(j, fmt, swiglu, m, n, k):
+    """Row counts that either kernel may take, by the sums that K is split into:
+    several row tiles with split sums, a ragged K, into a wider buffer whose
+    other columns and rows stay as they were."""
+    qa, qb, a, b = _operands(j, m, n, k, fmt)
+    cols = n // 2 if swiglu else n
+    buf = torch.full((m + 3, cols + 16), 7.0, dtype=torch.float32, device="cuda")
+    out = buf[1:m + 1, 8:8 + cols]
+    j.gemm_fp4(qa, qb, swiglu=swiglu, dtype=torch.float32, out=out)
+    got, y = out.double().cpu().numpy(), o.product(a, b)
+    tol = _tolerance(a, b, torch.float32, y)
+    if swiglu:  # as in test_gemm_swiglu, fp32 out
+        g, u, ref = y[:, :cols], y[:, cols:], o.product(a, b, True)
+        tol = 1.1 * tol[:, :cols] * np.abs(u) + np.abs(o.silu(g)) * tol[:, cols:] + np.abs(ref) * (2.0 ** -24 + 2.0 ** -20)
+        y = ref
+    assert np.all(np.abs(got - y) <= tol + 1e-30)
+    buf[1:m + 1, 8:8 + cols] = 7
+    assert torch.all(buf == 7)
