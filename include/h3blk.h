@@ -266,7 +266,11 @@ H3BLK_API int h3blk_gemm_bf16(int64_t M, int N, int K, const void* A, const void
  *              Bytes of blocks past K in a row's last atom are finite scales
  *              (never NaN); bytes of rows past the last are not written or used.
  *   row_scale  fp32 [rows]
- * Device pointers, caller-owned, 16-byte aligned. */
+ * Device pointers, caller-owned, 16-byte aligned.
+ * The kernels of these calls and of h3blk_sandwich_norm set themselves up while
+ * the kernel before them in the stream ends, and let one behind them that is
+ * launched with programmatic stream serialization do the same; such a kernel
+ * waits for theirs (griddepcontrol.wait) before it touches memory. */
 #define H3BLK_FP4_MX 0
 #define H3BLK_FP4_NV 1
 typedef struct {
