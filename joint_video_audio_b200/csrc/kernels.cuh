@@ -187,6 +187,7 @@ struct SandwichArgs {
   float* row_scale;
 };
 cudaError_t launch_sandwich(const SandwichArgs& a, int num_sms, cudaStream_t s);
+
 // CTAs of a kernel that an SM holds at once. The persistent row passes launch
 // exactly that many per SM: with fewer, the SMs that a preceding kernel leaves
 // first would fill up and take the work of those it leaves last.
@@ -231,6 +232,7 @@ struct ChainedLaunch {
       cfg.numAttrs = 2;
     }
   }
+  ChainedLaunch(const ChainedLaunch&) = delete;  // cfg points into it
 };
 
 // ---------------------------------------------------------------- attention
