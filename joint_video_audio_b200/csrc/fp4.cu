@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(GROUPED ? kGroupWarps * 32 : kMaxRowWarps * 32
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kMaxStages];
   __shared__ float red[2][kMaxRowWarps];
-  __shared__ int fail[2];
+  __shared__ int fail[2];  // by parity: a thread that is ahead sets the next group's
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = threadIdx.x & 3, g = lane >> 2;
   const int R = GROUPED ? kGroupWarps * 8 / pitch : 1;
@@ -135,7 +135,6 @@ __global__ void __launch_bounds__(GROUPED ? kGroupWarps * 32 : kMaxRowWarps * 32
       return;
     }
     if (threadIdx.x == 0) {
-      fail[par ^ 1] = 0;  // every thread passed the last group's check of that flag
       fence_proxy_async_smem();
       issue(grp + (int64_t)stages * gridDim.x, st);
     }

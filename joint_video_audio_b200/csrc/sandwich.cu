@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
   __shared__ float red[2][3][R][32];
   __shared__ int keys[kSortRows];
   __shared__ uint16_t ord[kSortRows];
-  __shared__ int fail[2];
+  __shared__ int fail[2];  // by parity: a thread that is ahead sets the next rows'
   const int lane = threadIdx.x & 31;
   const int nchunk = a.C >> 3;
   const uint32_t row_bytes = (uint32_t)a.C * 2u;
@@ -261,7 +261,6 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
         return;
       }
       if (threadIdx.x == 0) {
-        fail[par ^ 1] = 0;  // every thread passed the last rows' check of that flag
         fence_proxy_async_smem();
         issue(k + stages, st);
         if (cnt == 2) issue(k + 1 + stages, st + 1 == stages ? 0 : st + 1);
