@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const int4 tiw0 = __ldg(reinterpret_cast<const int4*>(p.tiles + kt));
       const int2 tiw1 = __ldg(reinterpret_cast<const int2*>(p.tiles + kt) + 2);
       const int kt_next = seq.at(j + 1, kt);
-      if (!mbar_wait(&s.s_full[t], j & 1, abort)) {
+      if (!mbar_wait_warp(&s.s_full[t], j & 1, abort)) {  // the reads below take the whole warp
         ok = false;
         break;
       }
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     if (!ok) {
       if (lane == 0) fail(p.err, abort);
-    } else if (mbar_wait(s.o_final, 0, abort)) {
+    } else if (mbar_wait_warp(s.o_final, 0, abort)) {
       tc_fence_after();
       const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
       __nv_bfloat16* dst;

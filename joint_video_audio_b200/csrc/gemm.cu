@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const TileCoord tc = tile_coord(t, tiles_m, tiles_n);
       const int buf = local & 1;
       const uint32_t use = (uint32_t)(local >> 1);
-      if (!mbar_wait(&s.tfull[buf], use & 1, abort)) {
+      if (!mbar_wait_warp(&s.tfull[buf], use & 1, abort)) {  // the reads below take the whole warp
         if (lane == 0) fail(s, p.err);
         break;
       }
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const TileCoord tc = tile_coord<kGroupNPair>(t, tiles_m, tiles_n);
       const int buf = local & 1;
       const uint32_t use = (uint32_t)(local >> 1);
-      if (!mbar_wait(&s.tfull[buf], use & 1, abort)) {
+      if (!mbar_wait_warp(&s.tfull[buf], use & 1, abort)) {  // the reads below take the whole warp
         if (lane == 0) fail_pair(s, p.err);
         break;
       }
@@ -731,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // neither CTA leaves while the other may still signal its barriers or read
   // its memory
+  __syncwarp();  // (lanes of the roles above come back one by one; the cluster's barrier takes whole warps)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();

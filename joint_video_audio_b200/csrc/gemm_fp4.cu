@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           row_b < rows_b ? __ldg(reinterpret_cast<const float4*>(p.b_row + row_b)) : make_float4(0.f, 0.f, 0.f, 0.f);
       const float ra = row0 + lane < p.M ? __ldg(p.a_row + row0 + lane) : 0.f;
       __syncwarp();
-      if (!mbar_wait(&tfull[buf], (uint32_t)(local >> 1) & 1, abort)) {
+      if (!mbar_wait_warp(&tfull[buf], (uint32_t)(local >> 1) & 1, abort)) {  // the reads below take the whole warp
         if (lane == 0) *abort = 1;
         break;
       }
@@ -777,6 +777,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
   // neither CTA leaves while the other may still signal its barriers or read
   // its memory: every signal has been waited for by now, so no ordering is needed
+  __syncwarp();  // (lanes of the roles above come back one by one; the cluster's barrier takes whole warps)
   tc_fence_before();
   cluster_sync_relaxed();
   tc_fence_after();
