@@ -301,10 +301,8 @@ cudaError_t launch_quant_t(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
   if (threads > 32 * kMaxRowWarps) return cudaErrorInvalidValue;
   const int stages = a.K <= 2048 ? kMaxStages : 3;
   const size_t smem = (size_t)stages * R * a.K * 2;
-  cudaError_t e;
-  if (smem > 40 * 1024 &&
-      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-    return e;
+  const cudaError_t e = smem > 40 * 1024 ? allow_smem<kern>(smem) : cudaSuccess;
+  if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)num_sms * resident_ctas<kern>(threads, smem);
   const int64_t groups = (a.rows + R - 1) / R, grid = groups < most ? groups : most;
   ChainedLaunch l(dim3((unsigned)grid), threads, smem, s);

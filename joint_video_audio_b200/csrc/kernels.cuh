@@ -188,16 +188,34 @@ struct SandwichArgs {
 };
 cudaError_t launch_sandwich(const SandwichArgs& a, int num_sms, cudaStream_t s);
 
-// CTAs of a kernel that an SM holds at once. The persistent row passes launch
-// exactly that many per SM: with fewer, the SMs that a preceding kernel leaves
-// first would fill up and take the work of those it leaves last.
+// A kernel's attributes, asked for once. (Registers as a bound where that fails.)
 template <auto kKernel>
-int resident_ctas(int threads, size_t smem) {
+const cudaFuncAttributes& kernel_attributes() {
   static const cudaFuncAttributes f = [] {
     cudaFuncAttributes a{};
     if (cudaFuncGetAttributes(&a, kKernel) != cudaSuccess) a.numRegs = 128;
     return a;
   }();
+  return f;
+}
+
+// Lets a kernel whose dynamic shared memory depends on the call be launched with
+// `smem` bytes of it: the limit always goes to the most that a CTA can have. Were
+// it the call's own size, a call of another thread could lower it between here
+// and the launch, which would then fail.
+template <auto kKernel>
+cudaError_t allow_smem(size_t smem) {
+  const size_t most = 227 * 1024 - kernel_attributes<kKernel>().sharedSizeBytes;
+  if (smem > most) return cudaErrorInvalidValue;
+  return cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
+// CTAs of a kernel that an SM holds at once. The persistent row passes launch
+// exactly that many per SM: with fewer, the SMs that a preceding kernel leaves
+// first would fill up and take the work of those it leaves last.
+template <auto kKernel>
+int resident_ctas(int threads, size_t smem) {
+  const cudaFuncAttributes& f = kernel_attributes<kKernel>();
   const int warps = (threads + 31) / 32;
   const int by_threads = 64 / warps;
   // a quarter of the SM has 16,384 registers and gives them out to warps, eight a thread at a time

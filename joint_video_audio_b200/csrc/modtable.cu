@@ -145,8 +145,8 @@ cudaError_t gemv_v(const WT* W, const float* b, int64_t wz, int64_t bz, int Z, i
                    const ModTimes& t, bool silu_in, bool silu_out, float alpha, bool acc, float* y, int64_t yz,
                    int64_t yv, int num_sms, cudaStream_t s) {
   const size_t smem = (size_t)V * I * sizeof(float);
-  auto k = gemv_sets_kernel<WT, V>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr auto k = gemv_sets_kernel<WT, V>;
+  cudaError_t e = allow_smem<k>(smem);
   if (e != cudaSuccess) return e;
   const int rows_per_block = (kGemvThreads / 32) * kRows;
   int blocks = (O + rows_per_block - 1) / rows_per_block;

@@ -469,16 +469,14 @@ __global__ void __launch_bounds__(WARPS * 32) rowring_kernel(const __nv_bfloat16
   if (threadIdx.x == 0) bulk_wait_all();
 }
 
-template <typename Kern>
-static cudaError_t persistent_grid(Kern kern, int threads, size_t smem, int64_t rows, int64_t* grid) {
+template <auto kKernel>
+static cudaError_t persistent_grid(int threads, size_t smem, int64_t rows, int64_t* grid) {
   cudaError_t e;
-  if (smem > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-    return e;
+  if (smem > 48 * 1024 && (e = allow_smem<kKernel>(smem)) != cudaSuccess) return e;
   int dev = 0, sms = 0, per_sm = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return e;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kKernel, threads, smem)) != cudaSuccess) return e;
   if (per_sm < 1) per_sm = 1;
   *grid = rows < (int64_t)sms * per_sm ? rows : (int64_t)sms * per_sm;
   return cudaSuccess;
@@ -492,7 +490,7 @@ static cudaError_t launch_rowring_t(const __nv_bfloat16* in, int64_t rows, int K
   stages = stages < 2 ? 2 : (stages > kRowMaxStages ? kRowMaxStages : stages);
   const size_t smem = (size_t)stages * row_bytes + 2 * out_bytes;
   int64_t grid = 0;
-  cudaError_t e = persistent_grid(rowring_kernel<WARPS, MODE>, WARPS * 32, smem, rows, &grid);
+  cudaError_t e = persistent_grid<rowring_kernel<WARPS, MODE>>(WARPS * 32, smem, rows, &grid);
   if (e != cudaSuccess) return e;
   rowring_kernel<WARPS, MODE><<<(unsigned)grid, WARPS * 32, smem, s>>>(in, rows, K, stages, q, sc, a, err);
   return cudaGetLastError();
@@ -648,12 +646,12 @@ __global__ void __launch_bounds__(THREADS) modnorm_stream_kernel(const __nv_bflo
 template <int CPT, int THREADS>
 static cudaError_t launch_rows_t(const __nv_bfloat16* in, int64_t rows, int K, __nv_bfloat16* out_h,
                                  const ModNormArgs& a, int* err, cudaStream_t s) {
-  auto kern = modnorm_stream_kernel<CPT, THREADS>;
+  constexpr auto kern = modnorm_stream_kernel<CPT, THREADS>;
   const size_t row_bytes = (size_t)K * 2;
   int stages = (int)(kStageBudget / row_bytes);
   stages = stages < 2 ? 2 : (stages > kMaxStages ? kMaxStages : stages);
   const size_t smem = (size_t)stages * row_bytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem<kern>(smem);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0, per_sm = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;

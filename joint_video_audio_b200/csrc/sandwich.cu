@@ -343,18 +343,16 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
 
 template <int HOUT, bool ROT, int CPT, int MAXT, int R>
 cudaError_t launch_t(const SandwichArgs& a, int num_sms, cudaStream_t s) {
-  auto kern = sandwich_kernel<HOUT, ROT, CPT, MAXT, R>;
+  constexpr auto kern = sandwich_kernel<HOUT, ROT, CPT, MAXT, R>;
   const int threads = ((a.C / 8 + CPT - 1) / CPT + 31) / 32 * 32;
   // up to eight rows ahead, three of the widest
   const size_t stage = (size_t)a.C * 4;
   int stages = (int)((a.C <= 2048 ? 32 * 1024 : 192 * 1024) / stage);
   stages = stages > kMaxStages ? kMaxStages : stages;
   const size_t smem = stages * stage;
-  cudaError_t e;
-  if (smem > 40 * 1024 &&
-      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-    return e;
-  const int64_t most = (int64_t)num_sms * resident_ctas<sandwich_kernel<HOUT, ROT, CPT, MAXT, R>>(threads, smem);
+  const cudaError_t e = smem > 40 * 1024 ? allow_smem<kern>(smem) : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)num_sms * resident_ctas<kern>(threads, smem);
   const int64_t grid = a.rows < most ? a.rows : most;
   ChainedLaunch l(dim3((unsigned)grid), threads, smem, s);
   return cudaLaunchKernelEx(&l.cfg, kern, a, stages, HOUT >= 2 ? fp4_katoms(HOUT == 3 ? kFp4NV : kFp4MX, a.C) : 0);

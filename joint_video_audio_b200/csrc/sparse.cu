@@ -177,7 +177,7 @@ cudaError_t launch_sparse_select(const SparseArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const size_t smem = (size_t)a.head_dim * 4 + (size_t)n_tiles * 8;
   if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = allow_smem<select_kernel>(smem);
     if (e != cudaSuccess) return e;
   }
   select_kernel<<<dim3((unsigned)n_blocks, (unsigned)a.heads), kSelThreads, smem, s>>>(
