@@ -50,3 +50,13 @@ def test_warps_are_whole_at_a_closing_cluster_barrier(name):
                 continue  # before the roles
             tail = head[head.rfind("__syncwarp()"):]
             assert "__syncwarp()" in head and "lane == 0" not in tail, f"{name}: {m.group(0)}"
+
+
+def test_the_abort_word_is_set_by_waits_alone():
+    """Every wait that succeeds passes over the abort word, so that setting it
+    stops nothing by itself: it is for those that gave up. The pair kernel's base
+    address 0 rests on its allocating all 512 columns, not on such a check."""
+    text = open(os.path.join(CSRC, "gemm_fp4.cu")).read()
+    assert "tmem_alloc_pair(tmem_slot, 512)" in text
+    for kernel in _body("gemm_fp4.cu"):
+        assert not re.search(r"if \(\*tmem_slot[^)]*\) \*?\w*abort", kernel)
