@@ -1,0 +1,61 @@
+"""4-bit products and dequantisation where their arithmetic is at its limits,
+against fp64."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import h3_fp4 as o
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def j():
+    assert torch.cuda.is_available(), "GPU tests need a B200"
+    import joint_video_audio_b200
+    return joint_video_audio_b200
+
+
+E2M1 = torch.tensor([.5, 1, 1.5, 2, 3, 4, 6, -.5, -1, -1.5, -2, -3, -4, -6])
+
+
+def wide_gates(m, f, seed):
+    """MX operands [m, 128] and [2 f, 128] whose values are multiples of a
+    quarter (gates) and of 2^-6 (ups), so that their fp32 sums are exact; the
+    gates reach past +-100."""
+    g = torch.Generator().manual_seed(seed)
+    a = E2M1[torch.randint(0, 14, (m, 128), generator=g)]
+    b = E2M1[torch.randint(0, 14, (2 * f, 128), generator=g)]
+    a[:, ::32], b[:, ::32] = 6, -6  # every block's scale is the table's own
+    a = a / 2
+    b[f:] /= 16
+    return a, b
+
+
+WIDE_GATES = [(5, 1024), (40, 512), (300, 256)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,f", WIDE_GATES)
+def test_swiglu_of_wide_gates(j, dtype, m, f):
+    """The product is exact, so that what is left is swiglu's own error: two units
+    of the last place each (2^-22) for the exponential, which enters numerator and
+    denominator by its factor, and for the quotient, one rounding (2^-24) each for
+    the sum, the products with g and with u; together below 2^-20, and the output
+    type's own. Where the output is bf16 the exponent -|g| log2 e is rounded to fp32:
+    half a step of up to 184 is 2^-17, times log 2, and the rounding of log2 e
+    itself another 128 * 2^-26: 2^-17 together. An exponential below the normals is
+    good to two of the smallest steps, and so are the products and the output."""
+    a, b = wide_gates(m, f, m + f)
+    ya = a.double().numpy() @ b.double().numpy().T
+    g, u = ya[:, :f], ya[:, f:]
+    assert g.min() < -100 and g.max() > 100 and ((g > -88.7) & (g < -87.4)).any()
+    ref = g / (1 + np.exp(-g)) * u
+    qa, qb = (j.quantize_fp4(v.to(torch.bfloat16).cuda(), "mx") for v in (a, b))
+    assert torch.equal(j.dequantize_fp4(qa).cpu().float(), a) and torch.equal(j.dequantize_fp4(qb).cpu().float(), b)
+    got = j.gemm_fp4(qa, qb, swiglu=True, dtype=dtype).double().cpu().numpy()
+    out = torch.finfo(dtype)
+    step = 2.0 ** -149 if dtype == torch.float32 else 2.0 ** -133
+    tol = np.abs(ref) * (out.eps / 2 + 2.0 ** -20 + (2.0 ** -17 if dtype == torch.bfloat16 else 0)) + 2.0 ** -147 * (np.abs(g) + 1) * (np.abs(u) + 1) + step
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), f"{bad.sum()} values, first at g = {g[bad][0]}, u = {u[bad][0]}: {got[bad][0]} not {ref[bad][0]}"
