@@ -297,14 +297,18 @@ H3BLK_API int h3blk_fp4_bytes(int format, int64_t rows, int K, size_t* codes, si
  * exactly, so codes and scales of given values are the same bits on any
  * implementation. rotate != 0 (K a multiple of 128) first applies the block-128
  * Hadamard transform of h3blk_rotate_quantize, its 1/sqrt(128) in row_scale.
- * A block that holds an infinity or a NaN (for rotate: whose 128 channels do)
- * gets the NaN scale; the other blocks are quantised as if it were zero.
+ * A block that holds an infinity or a NaN (for rotate: whose 128 channels do, or
+ * whose sums pass the largest float) gets the NaN scale; the other blocks are
+ * quantised as if it were zero.
  * UNSUPPORTED when K > 16384. */
 H3BLK_API int h3blk_quantize_fp4(const void* in_bf16, int64_t ld_in, int rotate, const h3blk_fp4* out, void* stream);
 
-/* The values `in` stands for (a rotated matrix stays rotated), rounded once to
- * the output type: H3BLK_BF16 or H3BLK_F32 [rows, K] with row stride ld_out
- * (>= K, a multiple of 8). */
+/* The values `in` stands for (a rotated matrix stays rotated), in the output
+ * type: H3BLK_BF16 or H3BLK_F32 [rows, K] with row stride ld_out (>= K, a
+ * multiple of 8). Code times block scale is exact; its product with row_scale is
+ * rounded to fp32, and from there to bf16, which for the row scales that
+ * h3blk_quantize_fp4 and h3blk_sandwich_norm write is the nearest bf16 (with one
+ * of the caller's own it may be the second nearest, next to a tie). */
 #define H3BLK_BF16 0
 #define H3BLK_F32 1
 H3BLK_API int h3blk_dequantize_fp4(const h3blk_fp4* in, int out_type, void* out, int64_t ld_out, void* stream);

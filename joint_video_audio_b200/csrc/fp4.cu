@@ -265,14 +265,17 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
     s0 = *fp4_scale_word(scales, row, katoms, 2 * blk);
     if (2 * blk + 1 < katoms) s1 = *fp4_scale_word(scales, row, katoms, 2 * blk + 1);
   }
-  const float rs = __ldg(row_scale + row);
+  float rs = __ldg(row_scale + row), eighth = 1.f;
+  // MX: a code times its block's scale, up to 6 * 2^127, may pass the largest float
+  // though the row's scale (1 / sqrt(128) where rotated) brings it back
+  if (FMT == kFp4MX && fabsf(rs) < 1.f) rs *= 8.f, eighth = 0.125f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (blk * 128 + j * 32 >= K) break;  // (K is a multiple of 32)
     // MX: block j; NV: blocks 2 j and 2 j + 1 of the 128 channels
     float sc[2];
     if (FMT == kFp4MX) {
-      sc[0] = sc[1] = e8m0_value((s0 >> (8 * j)) & 0xffu);
+      sc[0] = sc[1] = e8m0_value((s0 >> (8 * j)) & 0xffu) * eighth;
     } else {
       const uint32_t pair = (j < 2 ? s0 : s1) >> (16 * (j & 1));
       sc[0] = e4m3_value((pair >> (sizeof(T) == 2 ? 8 * (l >> 1) : 0)) & 0xffu);

@@ -59,3 +59,20 @@ def test_swiglu_of_wide_gates(j, dtype, m, f):
     tol = np.abs(ref) * (out.eps / 2 + 2.0 ** -20 + (2.0 ** -17 if dtype == torch.bfloat16 else 0)) + 2.0 ** -147 * (np.abs(g) + 1) * (np.abs(u) + 1) + step
     bad = np.abs(got - ref) > tol
     assert not bad.any(), f"{bad.sum()} values, first at g = {g[bad][0]}, u = {u[bad][0]}: {got[bad][0]} not {ref[bad][0]}"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_dequantize_rotated_values_near_the_largest_float(j, dtype):
+    """Rotated sums near 2^128 under a block scale of 2^126: code times scale is
+    2^128 there, the value 2^128 / sqrt(128) and finite. Two roundings of fp32 (the
+    product's and the row scale's), one of the output."""
+    x = torch.zeros(3, 256)
+    x[0, 0], x[0, 1] = 1.6e38, 1.4e38
+    x[1, 130], x[1, 131], x[1, 200] = -1.5e38, 1.1e38, -0.6e38
+    x = x.to(torch.bfloat16)
+    c, s, r, bad = o.quantize(x, "mx", True)
+    assert not bad.any() and s.max() == 253 and (c[s.repeat(32, 1) == 253] & 7).max() >= 6
+    ref = o.values(c, s, r, "mx")
+    assert np.abs(ref).max() < 2.0 ** 126
+    got = j.dequantize_fp4(j.quantize_fp4(x.cuda(), "mx", rotate=True), dtype).double().cpu().numpy()
+    assert np.all(np.abs(got - ref) <= np.abs(ref) * (2.0 ** -23 + torch.finfo(dtype).eps / 2))
