@@ -300,7 +300,8 @@ H3BLK_API int h3blk_fp4_bytes(int format, int64_t rows, int K, size_t* codes, si
  * A block that holds an infinity or a NaN (for rotate: whose 128 channels do, or
  * whose sums pass the largest float) gets the NaN scale; the other blocks are
  * quantised as if it were zero.
- * UNSUPPORTED when K > 16384. */
+ * The input and the parts of `out` must not overlap (INVALID_ARG). UNSUPPORTED
+ * when K > 16384. */
 H3BLK_API int h3blk_quantize_fp4(const void* in_bf16, int64_t ld_in, int rotate, const h3blk_fp4* out, void* stream);
 
 /* The values `in` stands for (a rotated matrix stays rotated), in the output
@@ -341,14 +342,15 @@ H3BLK_API int h3blk_gemm_fp4(const h3blk_fp4* A, const h3blk_fp4* B, int epilogu
  * feed-forward step. Rows with tag -1, and rows whose indices lie outside the
  * table, get zero gate, shift and scale (x_out = x).
  *   x, y, x_out  bf16 [n_rows, hidden], hidden a multiple of 128 (UNSUPPORTED
- *                otherwise, and above 16384); x_out may be x itself, and
- *                overlaps nothing else
+ *                otherwise, and above 16384); x_out may be x itself
  *   post_gain    bf16 [hidden], may be NULL (ones); only with post_norm
  *   norm_table   fp32 [n_tags][n_t][6][hidden]; NULL: no h is made
  *   h            bf16 [n_rows, hidden], or
  *   h_fp4        h as the operand of h3blk_gemm_fp4, quantised from its fp32
  *                values as by h3blk_quantize_fp4 (rotate as there). Exactly one
- *                of the two with norm_table, none without. */
+ *                of the two with norm_table, none without.
+ * x_out, h and the parts of h_fp4 overlap nothing else, one another neither
+ * (INVALID_ARG), but for x_out = x. */
 typedef struct {
   int64_t n_rows;
   int hidden, n_tags, n_t;

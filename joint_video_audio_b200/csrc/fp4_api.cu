@@ -30,20 +30,31 @@ int check_fp4(const h3blk_fp4* q) {
   return H3BLK_OK;
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na && nb && x < y + nb && y < x + na;
+struct Range {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
 }
-bool overlaps_fp4(const void* p, size_t n, const h3blk_fp4* q) {
-  return overlap(p, n, q->codes, (size_t)q->rows * (q->K / 2)) ||
-         overlap(p, n, q->scales, scale_bytes(q->format, q->rows, q->K)) ||
-         overlap(p, n, q->row_scale, (size_t)q->rows * 4);
+// The three buffers of a 4-bit matrix.
+struct Parts {
+  Range r[3];
+  explicit Parts(const h3blk_fp4* q)
+      : r{{q->codes, (size_t)q->rows * (q->K / 2)},
+          {q->scales, scale_bytes(q->format, q->rows, q->K)},
+          {q->row_scale, (size_t)q->rows * 4}} {}
+  bool overlap_one_another() const { return overlap(r[0], r[1]) || overlap(r[0], r[2]) || overlap(r[1], r[2]); }
+};
+bool overlaps_fp4(const Range& a, const h3blk_fp4* q) {
+  const Parts b(q);
+  return overlap(a, b.r[0]) || overlap(a, b.r[1]) || overlap(a, b.r[2]);
 }
 // Bytes spanned by `rows` rows of `cols` elements, `ld` elements apart.
 size_t span(int64_t rows, int64_t cols, int64_t ld, int esize) {
   return rows > 0 ? ((size_t)(rows - 1) * ld + cols) * esize : 0;
 }
-
 
 }  // namespace
 
@@ -65,7 +76,8 @@ int h3blk_quantize_fp4(const void* in, int64_t ld_in, int rotate, const h3blk_fp
   if (!in || !aligned16(in) || ld_in < out->K || ld_in % 8) return H3BLK_ERR_INVALID_ARG;
   if (rotate && out->K % 128) return H3BLK_ERR_INVALID_ARG;
   if (out->K > kMaxChannels) return H3BLK_ERR_UNSUPPORTED;
-  if (overlaps_fp4(in, span(out->rows, out->K, ld_in, 2), out)) return H3BLK_ERR_INVALID_ARG;
+  if (overlaps_fp4({in, span(out->rows, out->K, ld_in, 2)}, out) || Parts(out).overlap_one_another())
+    return H3BLK_ERR_INVALID_ARG;
   int sms = 0;
   PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
   st = h3api::device_info(&sms, &enc);
@@ -89,7 +101,7 @@ int h3blk_dequantize_fp4(const h3blk_fp4* in, int out_type, void* out, int64_t l
   if (out_type != H3BLK_BF16 && out_type != H3BLK_F32) return H3BLK_ERR_INVALID_ARG;
   if (!out || !aligned16(out) || ld_out < in->K || ld_out % 8) return H3BLK_ERR_INVALID_ARG;
   if (in->K > kMaxGemmK) return H3BLK_ERR_UNSUPPORTED;
-  if (overlaps_fp4(out, span(in->rows, in->K, ld_out, out_type == H3BLK_F32 ? 4 : 2), in)) return H3BLK_ERR_INVALID_ARG;
+  if (overlaps_fp4({out, span(in->rows, in->K, ld_out, out_type == H3BLK_F32 ? 4 : 2)}, in)) return H3BLK_ERR_INVALID_ARG;
   int sms = 0;
   PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
   st = h3api::device_info(&sms, &enc);
@@ -122,8 +134,8 @@ int h3blk_gemm_fp4(const h3blk_fp4* A, const h3blk_fp4* B, int epilogue, int out
   const int64_t N = swiglu ? B->rows / 2 : B->rows;
   if (!out || !aligned16(out) || ld_out < N || ld_out % 8) return H3BLK_ERR_INVALID_ARG;
   if (ld_out > kMaxStride) return H3BLK_ERR_UNSUPPORTED;
-  const size_t bytes = span(A->rows, N, ld_out, out_type == H3BLK_F32 ? 4 : 2);
-  if (overlaps_fp4(out, bytes, A) || overlaps_fp4(out, bytes, B)) return H3BLK_ERR_INVALID_ARG;
+  const Range written{out, span(A->rows, N, ld_out, out_type == H3BLK_F32 ? 4 : 2)};
+  if (overlaps_fp4(written, A) || overlaps_fp4(written, B)) return H3BLK_ERR_INVALID_ARG;
   int sms = 0;
   PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
   st = h3api::device_info(&sms, &enc);
@@ -158,19 +170,30 @@ int h3blk_sandwich_norm(const h3blk_sandwich* s, void* stream) {
   for (const void* p : ptrs)
     if (!aligned16(p)) return H3BLK_ERR_INVALID_ARG;
   if (s->hidden % 128 || s->hidden > kMaxChannels || s->n_rows > kMaxRows) return H3BLK_ERR_UNSUPPORTED;
-  const size_t bytes = (size_t)s->n_rows * s->hidden * 2;
-  if (overlap(s->x_out, bytes, s->y, bytes) || (s->x_out != s->x && overlap(s->x_out, bytes, s->x, bytes)))
-    return H3BLK_ERR_INVALID_ARG;
-  if (s->h && (overlap(s->h, bytes, s->x, bytes) || overlap(s->h, bytes, s->y, bytes) ||
-               overlap(s->h, bytes, s->x_out, bytes)))
-    return H3BLK_ERR_INVALID_ARG;
+  // what is written shares no byte with anything else, but for x_out = x
+  const size_t bytes = (size_t)s->n_rows * s->hidden * 2, channels = (size_t)s->hidden;
+  const unsigned __int128 table = (unsigned __int128)s->n_tags * s->n_t * 6 * channels * 4;
+  if (table >> 63) return H3BLK_ERR_INVALID_ARG;
+  const Range in[] = {{s->x, bytes},
+                      {s->y, bytes},
+                      {s->post_gain, channels * 2},
+                      {s->tag, (size_t)s->n_rows * 4},
+                      {s->tidx, (size_t)s->n_rows * 4},
+                      {s->mod_table, (size_t)table},
+                      {s->norm_table, (size_t)table}};
+  const Range x_out{s->x_out, bytes}, h{s->h, bytes};
+  for (const Range& r : in) {
+    const bool in_place = &r == in && s->x_out == s->x;
+    if ((overlap(x_out, r) && !in_place) || overlap(h, r)) return H3BLK_ERR_INVALID_ARG;
+  }
+  if (overlap(h, x_out)) return H3BLK_ERR_INVALID_ARG;
   if (s->h_fp4) {
     const int st = check_fp4(s->h_fp4);
     if (st != H3BLK_OK) return st;
     if (s->h_fp4->rows != s->n_rows || s->h_fp4->K != s->hidden) return H3BLK_ERR_INVALID_ARG;
-    if (overlaps_fp4(s->x, bytes, s->h_fp4) || overlaps_fp4(s->y, bytes, s->h_fp4) ||
-        overlaps_fp4(s->x_out, bytes, s->h_fp4))
-      return H3BLK_ERR_INVALID_ARG;
+    for (const Range& r : in)
+      if (overlaps_fp4(r, s->h_fp4)) return H3BLK_ERR_INVALID_ARG;
+    if (overlaps_fp4(x_out, s->h_fp4) || Parts(s->h_fp4).overlap_one_another()) return H3BLK_ERR_INVALID_ARG;
   }
   int sms = 0;
   PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
