@@ -3,7 +3,9 @@ shell (input projections, token refiner, block stack, heads) around it.
 
 The compute lives in libh3blk.so (hand-written sm_100a CUDA kernels behind the
 C-ABI declared in include/h3blk.h). This package is its ctypes binding and a
-thin torch-tensor wrapper; importing it fails if the library is not built.
+thin torch-tensor wrapper; importing it fails if the library is not built. The
+4-bit calls and the sandwich norm go through a native module of their own
+(_fp4_torch), which the first of them imports.
 """
 from ._binding import (  # noqa: F401
     EXPORTS, H3BLK_OK, H3BlkError, LIB_PATH, STAGE, STAGES, h3blk_config, h3blk_weights,

@@ -8,9 +8,27 @@ from functools import lru_cache
 import torch
 
 from . import _binding as B
-from . import _fp4_torch as _host
 
-_host.set_error(B.H3BlkError)
+
+class _Host:
+    """The calls of csrc/fp4_torch.cpp. Its module is tied to one Python and one
+    torch, so that it is imported with the first 4-bit call: the rest of the package
+    does without."""
+
+    def __getattr__(self, name):
+        if name.startswith("_"):
+            raise AttributeError(name)
+        try:
+            from . import _fp4_torch as m
+        except ImportError as e:
+            raise ImportError("the 4-bit calls need joint_video_audio_b200/_fp4_torch, built for this Python and torch "
+                              f"(python joint_video_audio_b200/build.py): {e}") from e
+        m.set_error(B.H3BlkError)
+        self.__dict__.update({k: f for k, f in vars(m).items() if not k.startswith("_")})
+        return self.__dict__[name]
+
+
+_host = _Host()
 FORMATS = {"mx": B.H3BLK_FP4_MX, "nv": B.H3BLK_FP4_NV}
 _IS_F32 = {torch.bfloat16: False, torch.float32: True}
 
