@@ -43,7 +43,7 @@ def _sources():
 
 
 def _headers():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+    return sorted(f for d, ext in ((CSRC, "*.cuh"), (CSRC, "*.h"), (INCLUDE, "*.h")) for f in glob.glob(os.path.join(d, ext)))
 
 
 def _stale(target, deps):
@@ -65,12 +65,22 @@ def _compile(src, verbose):
     return obj
 
 
+def _module_stamp(torch):
+    """What the module is built with: which Python, which torch and where."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return "\n".join([str(sysconfig.get_config_var("SOABI")), sys.version, torch, f.read()])
+
+
 def _build_module(force):
     src = os.path.join(CSRC, "fp4_torch.cpp")
     torch = os.path.dirname(find_spec("torch").origin)
-    version = os.path.join(torch, "version.py")  # another torch, another module
-    if not force and not _stale(MODULE, [src, version] + _headers()):
-        return
+    # dates do not tell one environment from another: what was built with is kept
+    # beside the objects and compared
+    stamp, stamp_file = _module_stamp(torch), os.path.join(OBJDIR, "_fp4_torch.stamp")
+    if not force and os.path.exists(stamp_file) and not _stale(MODULE, [src] + _headers()):
+        with open(stamp_file) as f:
+            if f.read() == stamp:
+                return
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = MODULE + ".tmp"
     inc = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
@@ -82,7 +92,11 @@ def _build_module(force):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(stamp_file):  # (a stamp never stands beside another module than its own)
+        os.remove(stamp_file)
     os.replace(tmp, MODULE)
+    with open(stamp_file, "w") as f:
+        f.write(stamp)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
