@@ -321,9 +321,7 @@ H3BLK_API int h3blk_dequantize_fp4(const h3blk_fp4* in, int out_type, void* out,
  *                     [A->rows, F], F = B->rows / 2 (the layout of w13)
  * A->rows may be 0. UNSUPPORTED unless the output's columns are a multiple of
  * 8 (STORE) or 128 (SWIGLU). `out` must not overlap the operands. Both operands
- * are rotated or neither is (not checked here). As with the other kernel-level
- * calls, a pipeline wait that runs out (2 s) ends the kernel with its output
- * incomplete, and nothing reports it. */
+ * are rotated or neither is (not checked here). */
 #define H3BLK_FP4_STORE 0
 #define H3BLK_FP4_SWIGLU 1
 H3BLK_API int h3blk_gemm_fp4(const h3blk_fp4* A, const h3blk_fp4* B, int epilogue, int out_type, void* out,
@@ -365,6 +363,13 @@ typedef struct {
   int rotate;
 } h3blk_sandwich;
 H3BLK_API int h3blk_sandwich_norm(const h3blk_sandwich* args, void* stream);
+
+/* Device status of the 4-bit calls and the sandwich norm: synchronises `stream`
+ * and sets *status to H3BLK_ERR_TIMEOUT if a kernel of theirs on the current
+ * device gave up a pipeline wait (2 s) since the last check, and its output is
+ * incomplete, else to H3BLK_OK. Covers the calls of every stream that have ended
+ * by then, and the replays of captured ones; not to be called under capture. */
+H3BLK_API int h3blk_fp4_check(void* stream, int* status);
 
 /* ------------------------------------------------- modulation-table producer */
 /* The step before the block: turns the distinct timesteps of a forward into the
@@ -591,6 +596,11 @@ H3BLK_API int h3blk_attention_noalloc_check(void* stream, int* status);
  * caller-owned device int32 (4-byte aligned) used as the error word; it is
  * reset by the call. INVALID_ARG for a null pointer or a limit out of range. */
 H3BLK_API int h3blk_selftest_wait(int complete, int limit_ms, void* word, void* stream, int* status);
+
+/* Test-only: a kernel on `stream` whose one bounded wait runs out after limit_ms
+ * milliseconds (1..2000) and is reported as those of the 4-bit calls are
+ * (h3blk_fp4_check). The kernel returns normally. */
+H3BLK_API int h3blk_selftest_fp4_wait(int limit_ms, void* stream);
 
 /* Message for a status code (static storage). */
 H3BLK_API const char* h3blk_error_string(int status);

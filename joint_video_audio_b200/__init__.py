@@ -15,6 +15,6 @@ from .block import (  # noqa: F401
     DeviceWeights, H3Block, ModulationWeights, gemm_bf16, gemm_s8_s32, make_config, modulation_table, rotate_quantize,
 )
 from .fp4 import (  # noqa: F401
-    Fp4Tensor, dequantize_fp4, gemm_fp4, quantize_fp4, sandwich_norm,
+    Fp4Tensor, check_fp4, dequantize_fp4, gemm_fp4, quantize_fp4, sandwich_norm,
 )
 from .model import DeviceInputs, DeviceModel, Model, ModelGraph  # noqa: F401

@@ -34,7 +34,7 @@ EXPORTS = ["h3blk_create", "h3blk_destroy", "h3blk_workspace_bytes", "h3blk_stag
            "h3blk_ulysses_buffer_bytes", "h3blk_ulysses_workspace_bytes", "h3blk_ulysses_qkv",
            "h3blk_ulysses_attention", "h3blk_ulysses_out", "h3blk_set_attention_density",
            "h3blk_selftest_wait", "h3blk_set_debug_accumulators", "h3blk_fp4_bytes", "h3blk_quantize_fp4",
-           "h3blk_dequantize_fp4", "h3blk_gemm_fp4", "h3blk_sandwich_norm"]
+           "h3blk_dequantize_fp4", "h3blk_gemm_fp4", "h3blk_sandwich_norm", "h3blk_fp4_check", "h3blk_selftest_fp4_wait"]
 
 H3BLK_FP4_MX, H3BLK_FP4_NV = 0, 1
 H3BLK_BF16, H3BLK_F32 = 0, 1
@@ -141,6 +141,8 @@ def _load():
         "h3blk_dequantize_fp4": (i32, [vp, i32, vp, i64, vp]),
         "h3blk_gemm_fp4": (i32, [vp, vp, i32, i32, vp, i64, vp]),
         "h3blk_sandwich_norm": (i32, [vp, vp]),
+        "h3blk_fp4_check": (i32, [vp, C.POINTER(i32)]),
+        "h3blk_selftest_fp4_wait": (i32, [i32, vp]),
         "h3blk_error_string": (C.c_char_p, [i32]),
         "h3blk_version": (i32, []),
         "h3blk_set_kernel_events": (i32, [vp, C.POINTER(vp), i32]),
@@ -294,6 +296,18 @@ def h3blk_gemm_fp4(a: h3blk_fp4, b: h3blk_fp4, epilogue, out_type, out, ld_out, 
 
 def h3blk_sandwich_norm(args: h3blk_sandwich, stream) -> int:
     return _lib.h3blk_sandwich_norm(_ref(args), stream)
+
+
+def h3blk_fp4_check(stream) -> int:
+    """Synchronises `stream`; device status of the 4-bit calls and the sandwich
+    norm since the last check (H3BLK_OK or H3BLK_ERR_TIMEOUT)."""
+    st = C.c_int(-1)
+    _check("h3blk_fp4_check", _lib.h3blk_fp4_check(stream, C.byref(st)))
+    return st.value
+
+
+def h3blk_selftest_fp4_wait(limit_ms, stream) -> int:
+    return _lib.h3blk_selftest_fp4_wait(limit_ms, stream)
 
 
 def h3blk_set_kernel_events(handle, events) -> None:

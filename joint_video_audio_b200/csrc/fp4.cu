@@ -47,7 +47,8 @@ __device__ __forceinline__ float warp_max(float v) {  // of values that are not 
 template <int FMT, bool ROT, bool GROUPED>
 __global__ void __launch_bounds__(GROUPED ? kGroupWarps * 32 : kMaxRowWarps * 32, GROUPED ? 7 : 2)
     quantize_fp4_kernel(const __nv_bfloat16* __restrict__ in, int64_t ld, int64_t rows, int K, int katoms, int stages,
-                        int pitch, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, float* __restrict__ row_scale) {
+                        int pitch, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, float* __restrict__ row_scale,
+                        int* err) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kMaxStages];
   __shared__ float red[2][kMaxRowWarps];
@@ -127,11 +128,13 @@ __global__ void __launch_bounds__(GROUPED ? kGroupWarps * 32 : kMaxRowWarps * 32
     }
     __syncthreads();  // every thread has read the slot
     if (fail[par]) {  // a load never landed: those in flight must before the CTA's shared memory goes
-      if (threadIdx.x == 0)
+      if (threadIdx.x == 0) {
+        atomicOr(err, kErrTimeoutStream);
         for (int i = 0; i < stages && grp + (int64_t)i * gridDim.x < groups; ++i) {
           mbar_wait(&full[st], phase, nullptr);
           if (++st == stages) st = 0, phase ^= 1;
         }
+      }
       return;
     }
     if (threadIdx.x == 0) {
@@ -310,7 +313,7 @@ cudaError_t launch_quant_t(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
   const int64_t groups = (a.rows + R - 1) / R, grid = groups < most ? groups : most;
   ChainedLaunch l(dim3((unsigned)grid), threads, smem, s);
   return cudaLaunchKernelEx(&l.cfg, kern, a.in, a.ld, a.rows, a.K, fp4_katoms(FMT, a.K), stages, pitch, a.codes, a.scales,
-                            a.row_scale);
+                            a.row_scale, a.err);
 }
 
 template <int FMT, bool ROT>

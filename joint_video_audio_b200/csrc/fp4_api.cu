@@ -3,10 +3,16 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "api_internal.h"
 #include "fp4.cuh"
 
 namespace {
+// What the kernels of these calls report, on each device: a bit per kind of wait
+// that ran out, until h3blk_fp4_check takes it.
+__device__ int g_fp4_error;
+
 using h3api::aligned16;
 using h3api::cuda_status;
 
@@ -51,6 +57,42 @@ bool overlaps_fp4(const Range& a, const h3blk_fp4* q) {
   const Parts b(q);
   return overlap(a, b.r[0]) || overlap(a, b.r[1]) || overlap(a, b.r[2]);
 }
+// The current device's error word, and what launches need besides.
+struct Device {
+  int sms = 0;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  int* err = nullptr;
+};
+int device(Device* d) {
+  constexpr int kMaxDevices = 64;
+  static std::mutex mu;
+  static int* words[kMaxDevices];
+  const int st = h3api::device_info(&d->sms, &d->encode);
+  if (st != H3BLK_OK) return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return H3BLK_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!words[dev]) {
+    // (may load the module, which a capture under way on another stream would refuse)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return H3BLK_ERR_CUDA;
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_fp4_error);
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess || e != cudaSuccess || !p) return H3BLK_ERR_CUDA;
+    words[dev] = static_cast<int*>(p);
+  }
+  d->err = words[dev];
+  return H3BLK_OK;
+}
+
+// A wait of the kind that these calls' kernels make, which runs out.
+__global__ void late_wait_kernel(unsigned long long limit_ns, int* err) {
+  __shared__ uint64_t bar;
+  h3::mbar_init(&bar, 1);
+  h3::fence_mbar_init();
+  if (!h3::mbar_wait_for(&bar, 0, nullptr, limit_ns)) atomicOr(err, h3::kErrTimeoutStream);
+}
+
 // Bytes spanned by `rows` rows of `cols` elements, `ld` elements apart.
 size_t span(int64_t rows, int64_t cols, int64_t ld, int esize) {
   return rows > 0 ? ((size_t)(rows - 1) * ld + cols) * esize : 0;
@@ -78,9 +120,8 @@ int h3blk_quantize_fp4(const void* in, int64_t ld_in, int rotate, const h3blk_fp
   if (out->K > kMaxChannels) return H3BLK_ERR_UNSUPPORTED;
   if (overlaps_fp4({in, span(out->rows, out->K, ld_in, 2)}, out) || Parts(out).overlap_one_another())
     return H3BLK_ERR_INVALID_ARG;
-  int sms = 0;
-  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  st = h3api::device_info(&sms, &enc);
+  Device d;
+  st = device(&d);
   if (st != H3BLK_OK) return st;
   h3::Fp4QuantArgs a;
   a.in = static_cast<const __nv_bfloat16*>(in);
@@ -92,7 +133,8 @@ int h3blk_quantize_fp4(const void* in, int64_t ld_in, int rotate, const h3blk_fp
   a.codes = static_cast<uint8_t*>(out->codes);
   a.scales = static_cast<uint8_t*>(out->scales);
   a.row_scale = out->row_scale;
-  return cuda_status(h3::launch_quantize_fp4(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+  a.err = d.err;
+  return cuda_status(h3::launch_quantize_fp4(a, d.sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int h3blk_dequantize_fp4(const h3blk_fp4* in, int out_type, void* out, int64_t ld_out, void* stream) {
@@ -102,9 +144,8 @@ int h3blk_dequantize_fp4(const h3blk_fp4* in, int out_type, void* out, int64_t l
   if (!out || !aligned16(out) || ld_out < in->K || ld_out % 8) return H3BLK_ERR_INVALID_ARG;
   if (in->K > kMaxGemmK) return H3BLK_ERR_UNSUPPORTED;
   if (overlaps_fp4({out, span(in->rows, in->K, ld_out, out_type == H3BLK_F32 ? 4 : 2)}, in)) return H3BLK_ERR_INVALID_ARG;
-  int sms = 0;
-  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  st = h3api::device_info(&sms, &enc);
+  Device d;
+  st = device(&d);
   if (st != H3BLK_OK) return st;
   h3::Fp4DequantArgs a;
   a.codes = static_cast<const uint8_t*>(in->codes);
@@ -136,9 +177,8 @@ int h3blk_gemm_fp4(const h3blk_fp4* A, const h3blk_fp4* B, int epilogue, int out
   if (ld_out > kMaxStride) return H3BLK_ERR_UNSUPPORTED;
   const Range written{out, span(A->rows, N, ld_out, out_type == H3BLK_F32 ? 4 : 2)};
   if (overlaps_fp4(written, A) || overlaps_fp4(written, B)) return H3BLK_ERR_INVALID_ARG;
-  int sms = 0;
-  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  st = h3api::device_info(&sms, &enc);
+  Device d;
+  st = device(&d);
   if (st != H3BLK_OK) return st;
   h3::Fp4GemmArgs g;
   g.a_codes = static_cast<const uint8_t*>(A->codes);
@@ -155,7 +195,8 @@ int h3blk_gemm_fp4(const h3blk_fp4* A, const h3blk_fp4* B, int epilogue, int out
   g.f32 = out_type == H3BLK_F32;
   g.out = out;
   g.ld = ld_out;
-  return cuda_status(h3::launch_gemm_fp4(g, enc, sms, reinterpret_cast<cudaStream_t>(stream)));
+  g.err = d.err;
+  return cuda_status(h3::launch_gemm_fp4(g, d.encode, d.sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int h3blk_sandwich_norm(const h3blk_sandwich* s, void* stream) {
@@ -195,9 +236,8 @@ int h3blk_sandwich_norm(const h3blk_sandwich* s, void* stream) {
       if (overlaps_fp4(r, s->h_fp4)) return H3BLK_ERR_INVALID_ARG;
     if (overlaps_fp4(x_out, s->h_fp4) || Parts(s->h_fp4).overlap_one_another()) return H3BLK_ERR_INVALID_ARG;
   }
-  int sms = 0;
-  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  const int st = h3api::device_info(&sms, &enc);
+  Device d;
+  const int st = device(&d);
   if (st != H3BLK_OK) return st;
   h3::SandwichArgs a{};
   a.x = static_cast<const __nv_bfloat16*>(s->x);
@@ -219,6 +259,7 @@ int h3blk_sandwich_norm(const h3blk_sandwich* s, void* stream) {
   a.branch_scale = s->branch_scale;
   a.x_out = static_cast<__nv_bfloat16*>(s->x_out);
   a.h = static_cast<__nv_bfloat16*>(s->h);
+  a.err = d.err;
   if (s->h_fp4) {
     a.nv = s->h_fp4->format == H3BLK_FP4_NV;
     a.rotate = s->rotate != 0;
@@ -226,7 +267,33 @@ int h3blk_sandwich_norm(const h3blk_sandwich* s, void* stream) {
     a.scales = static_cast<uint8_t*>(s->h_fp4->scales);
     a.row_scale = s->h_fp4->row_scale;
   }
-  return cuda_status(h3::launch_sandwich(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(h3::launch_sandwich(a, d.sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int h3blk_fp4_check(void* stream, int* status) {
+  if (!status) return H3BLK_ERR_INVALID_ARG;
+  Device d;
+  const int st = device(&d);
+  if (st != H3BLK_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int bits = 0;
+  if (cudaMemcpyAsync(&bits, d.err, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return H3BLK_ERR_CUDA;
+  // (cleared only where something stood: a report that comes in between is not lost)
+  if (bits && (cudaMemsetAsync(d.err, 0, sizeof(int), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess))
+    return H3BLK_ERR_CUDA;
+  *status = bits ? H3BLK_ERR_TIMEOUT : H3BLK_OK;
+  return H3BLK_OK;
+}
+
+int h3blk_selftest_fp4_wait(int limit_ms, void* stream) {
+  if (limit_ms < 1 || limit_ms > 2000) return H3BLK_ERR_INVALID_ARG;
+  Device d;
+  const int st = device(&d);
+  if (st != H3BLK_OK) return st;
+  late_wait_kernel<<<1, 1, 0, reinterpret_cast<cudaStream_t>(stream)>>>((unsigned long long)limit_ms * 1000000ull, d.err);
+  return cuda_status(cudaGetLastError());
 }
 
 }  // extern "C"

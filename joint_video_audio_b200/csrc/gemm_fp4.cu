@@ -67,6 +67,12 @@ __device__ __forceinline__ float swiglu(float g, float u) {
   return (g < 0.f ? g * e : g) * rcp_approx(1.f + e) * u;
 }
 
+// A wait ran out: the CTA's others stop, and the host can learn of it.
+__device__ __forceinline__ void give_up(volatile int* abort, int* err) {
+  *abort = 1;
+  atomicOr(err, kErrTimeoutGemm);
+}
+
 // ------------------------------------------------------------------ few rows
 constexpr int kFewThreads = 192;
 constexpr int kMaxSplit = 6;  // CTAs that share a product's K
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(kFewThreads)
       int issued = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1, vabort)) {
-          *vabort = 1;
+          give_up(vabort, p.err);
           break;
         }
         uint8_t* st = smem + (size_t)stage * Cfg::kStageBytes;
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(kFewThreads)
           stage = kStages - 1;
           phase ^= 1;
         }
-        mbar_wait(&full[stage], phase, nullptr);
+        if (!mbar_wait(&full[stage], phase, nullptr)) give_up(vabort, p.err);
       }
     }
   } else if (warp == 1) {
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kFewThreads)
       const bool r0 = mbar_try_wait(&full[stage], phase), r1 = mbar_try_wait(&sfree[buf], sfree_parity);
       if (!__all_sync(0xffffffffu, r0 && r1) &&
           !(mbar_wait_warp(&full[stage], phase, vabort) && mbar_wait_warp(&sfree[buf], sfree_parity, vabort))) {
-        if (lane == 0) *vabort = 1;
+        if (lane == 0) give_up(vabort, p.err);
         ok = false;
         break;
       }
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kFewThreads)
     // issued has ended) once tfull flips
     mma_commit_w(tfull);
     mbar_wait(tfull, 0, nullptr);
-    if (!ok && lane == 0) *vabort = 1;
+    if (!ok && lane == 0) give_up(vabort, p.err);
   }
   __syncwarp();
   // ------------------------------------------------------------------ epilogue
@@ -309,6 +315,7 @@ __global__ void __launch_bounds__(kFewThreads)
       if (NW == 2) ru = __ldg(reinterpret_cast<const float4*>(p.b_row + p.N + n));
     }
     good = __all_sync(0xffffffffu, mbar_wait(tfull, 0, nullptr) && !*vabort);
+    if (!good && lane == 0) give_up(vabort, p.err);
     tc_fence_after();
     const int quad = warp & 3;
     const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16);
@@ -323,6 +330,7 @@ __global__ void __launch_bounds__(kFewThreads)
       }
     }
   }
+  __syncwarp();
   if (split > 1)
     cluster_sync();
   else
@@ -624,7 +632,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int b0 = SWIGLU ? tc.n * 128 : tc.n * 256, b1 = SWIGLU ? p.N + b0 : b0 + 128;
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort)) {
-            *abort = 1;
+            give_up(abort, p.err);
             ok = false;
             break;
           }
@@ -652,7 +660,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             stage = kStages - 1;
             phase ^= 1;
           }
-          mbar_wait(&full[stage], phase, nullptr);
+          if (!mbar_wait(&full[stage], phase, nullptr)) give_up(abort, p.err);
         }
       }
     }
@@ -665,7 +673,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       bool ok = true;
       for (int t = cluster; t < num_tiles && ok; t += n_clusters, ++local) {
         if (local > 0 && !mbar_wait_warp(tempty, (uint32_t)(local - 1) & 1, abort)) {
-          if (lane == 0) *abort = 1;
+          if (lane == 0) give_up(abort, p.err);
           break;
         }
         tc_fence_after();
@@ -713,17 +721,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         }
         if (!ok) {
-          if (lane == 0) *abort = 1;
+          if (lane == 0) give_up(abort, p.err);
         } else {
           mma_commit_pair_w(&tfull[local & 1], 0x3);
         }
       }
       mma_commit_pair_w(drain, 0x3);
-      mbar_wait(drain, 0, nullptr);
+      if (!mbar_wait(drain, 0, nullptr)) give_up(abort, p.err);
     } else if (lane == 0) {
       // second CTA: its shared and tensor memory serve the pair's products
       // until the last one completes
-      mbar_wait(drain, 0, nullptr);
+      if (!mbar_wait(drain, 0, nullptr)) give_up(abort, p.err);
     }
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
@@ -747,7 +755,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const float ra = row0 + lane < p.M ? __ldg(p.a_row + row0 + lane) : 0.f;
       __syncwarp();
       if (!mbar_wait_warp(&tfull[buf], (uint32_t)(local >> 1) & 1, abort)) {  // the reads below take the whole warp
-        if (lane == 0) *abort = 1;
+        if (lane == 0) give_up(abort, p.err);
         break;
       }
       tc_fence_after();

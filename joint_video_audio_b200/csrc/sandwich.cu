@@ -253,11 +253,13 @@ __global__ void __launch_bounds__(MAXT) sandwich_kernel(const SandwichArgs a, in
       // CTA stops because a load never landed
       cta_reduce<false, R>(ss, rd[0]);
       if (fail[par]) {
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0) {
+          atomicOr(a.err, kErrTimeoutStream);
           for (int i = k; i < k + stages && i < n; ++i) {
             mbar_wait(&full[st], phase, nullptr);
             if (++st == stages) st = 0, phase ^= 1;
           }
+        }
         return;
       }
       if (threadIdx.x == 0) {

@@ -155,3 +155,12 @@ def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post
     if out is not None and h != "bf16":
         out = _matrix(h, tuple(x.shape), bool(rotate), out)
     return x_out, out
+
+
+def check_fp4(device=None) -> int:
+    """Device status of the 4-bit calls and the sandwich norm on `device` (the
+    current one) since the last check, behind a synchronisation with its current
+    stream: H3BLK_OK, or H3BLK_ERR_TIMEOUT if a kernel gave up a wait and left its
+    output incomplete. h3blk_fp4_check."""
+    with torch.cuda.device(device):
+        return B.h3blk_fp4_check(torch.cuda.current_stream().cuda_stream)
