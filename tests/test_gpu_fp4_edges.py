@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from oracle import h3_fp4 as o
+from tests.test_gpu_fp4 import _operands, _tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,30 @@ def test_dequantize_rotated_values_near_the_largest_float(j, dtype):
     assert np.abs(ref).max() < 2.0 ** 126
     got = j.dequantize_fp4(j.quantize_fp4(x.cuda(), "mx", rotate=True), dtype).double().cpu().numpy()
     assert np.all(np.abs(got - ref) <= np.abs(ref) * (2.0 ** -23 + torch.finfo(dtype).eps / 2))
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n,k,swiglu", [(1, 512, 5376, True), (17, 512, 5472, True), (50, 1024, 4128, True), (64, 256, 7168, True),
+                                          (20, 256, 2048, False), (33, 384, 2080, False)])
+def test_few_rows_with_split_sums(j, fmt, dtype, m, n, k, swiglu):
+    """Up to 64 rows whose K several CTAs share, at each of the kernel's widths
+    (16, 32, 64 rows), into a wider buffer whose other bytes stay as they were.
+    Bounds as for the other products, with silu' <= 1.1 and swiglu's own error
+    (test_swiglu_of_wide_gates) below 2^-17 (bf16) and 2^-20 (fp32)."""
+    qa, qb, a, b = _operands(j, m, n, k, fmt)
+    cols = n // 2 if swiglu else n
+    buf = torch.full((m + 3, cols + 16), 7.0, dtype=dtype, device="cuda")
+    out = buf[1:m + 1, 8:8 + cols]
+    j.gemm_fp4(qa, qb, swiglu=swiglu, dtype=dtype, out=out)
+    got, y = out.double().cpu().numpy(), o.product(a, b)
+    if swiglu:
+        t = _tolerance(a, b, torch.float32, y)
+        g, u, y = y[:, :cols], y[:, cols:], o.product(a, b, True)
+        own = 2.0 ** -17 if dtype == torch.bfloat16 else 2.0 ** -20
+        tol = 1.1 * t[:, :cols] * np.abs(u) + np.abs(o.silu(g)) * t[:, cols:] + np.abs(y) * (torch.finfo(dtype).eps / 2 + own) + 1e-30
+    else:
+        tol = _tolerance(a, b, dtype, y)
+    assert np.all(np.abs(got - y) <= tol)
+    out.fill_(7)
+    assert torch.all(buf == 7)
