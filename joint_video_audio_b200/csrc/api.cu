@@ -60,6 +60,10 @@ int device_info(int* num_sms, PFN_cuTensorMapEncodeTiled_v12000* encode) {
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? H3BLK_OK : H3BLK_ERR_CUDA; }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -71,11 +75,7 @@ using h3api::aligned16;
 using h3api::align256;
 using h3api::cuda_status;
 using h3api::device_info;
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
+using h3api::overlap;
 
 // Workspace layout: every stage buffer at a 256-byte aligned offset.
 struct Layout {

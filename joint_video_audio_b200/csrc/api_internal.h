@@ -25,6 +25,8 @@ namespace h3api {
 // unless the device is sm_100.
 int device_info(int* num_sms, PFN_cuTensorMapEncodeTiled_v12000* encode);
 bool aligned16(const void* p);
+// Whether two buffers share a byte (none with a null or an empty one).
+bool overlap(const void* a, size_t na, const void* b, size_t nb);
 size_t align256(size_t v);
 int cuda_status(cudaError_t e);
 

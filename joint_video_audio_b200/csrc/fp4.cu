@@ -16,12 +16,6 @@ constexpr int kMaxRowWarps = 16;  // 1024 channels each: K <= 16384
 constexpr int kGroupWarps = 4;    // of a group of narrow rows
 constexpr int kMaxStages = 4;
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 __device__ __forceinline__ float warp_max(float v) {  // of values that are not negative
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }

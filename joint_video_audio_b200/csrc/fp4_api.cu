@@ -40,10 +40,7 @@ struct Range {
   const void* p;
   size_t n;
 };
-bool overlap(const Range& a, const Range& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
-}
+bool overlap(const Range& a, const Range& b) { return h3api::overlap(a.p, a.n, b.p, b.n); }
 // The three buffers of a 4-bit matrix.
 struct Parts {
   Range r[3];

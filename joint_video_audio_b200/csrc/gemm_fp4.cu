@@ -515,15 +515,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
                "r"(smem_u32(src)), "r"(x), "r"(y)
                : "memory");
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // One epilogue warp's unit: lane's row of v, as T, to the unit with the
 // 128-byte swizzle, then stored at column x, row y where that lies inside.
 template <typename T>
 __device__ __forceinline__ void store_unit(uint8_t* unit, const CUtensorMap* m, int lane, const float* v, int x, int64_t y,
                                            const Fp4GemmArgs& p) {
-  if (lane == 0) bulk_wait_read();  // the unit's last store has read it
+  if (lane == 0) bulk_wait_read<0>();  // the unit's last store has read it
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -798,7 +796,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait_read();  // the output has left shared memory (it reaches the matrix before the grid ends)
+    if (lane == 0) bulk_wait_read<0>();  // the output has left shared memory (it reaches the matrix before the grid ends)
   }
   // neither CTA leaves while the other may still signal its barriers or read
   // its memory: every signal has been waited for by now, so no ordering is needed

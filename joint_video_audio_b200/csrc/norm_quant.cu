@@ -168,26 +168,6 @@ constexpr int kRowRingBudget = 32 * 1024;  // shared-memory bytes of one CTA's i
 constexpr int kRowMaxStages = 8;
 constexpr int kRowSortChunk = 512;         // rows sorted by key at a time
 
-__device__ __forceinline__ void bulk_store(void* gdst, const void* ssrc, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(gdst)),
-               "r"(smem_u32(ssrc)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// every committed bulk store but the newest N has finished reading shared memory
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-// every committed bulk store has completed
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-__device__ __forceinline__ void bulk_load_row(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // ---- row ring: shared-memory layout of a thread's channels
 // Thread t owns channels [32 t, 32 t + 32) as four 8-channel chunks. Its
 // register slot j holds chunk j ^ r, r = ((t >> 1) ^ (t >> 3)) & 3: the
@@ -351,7 +331,7 @@ __global__ void __launch_bounds__(WARPS * 32) rowring_kernel(const __nv_bfloat16
       if (kk >= kend) return;
       const int st = (int)(kk % stages);
       mbar_expect_tx(&full[st], row_bytes);
-      bulk_load_row(ring + (size_t)st * row_bytes, in + row_of(kk) * (int64_t)K, row_bytes, &full[st]);
+      bulk_load(ring + (size_t)st * row_bytes, in + row_of(kk) * (int64_t)K, row_bytes, &full[st]);
     };
     if (threadIdx.x == 0) {
       fence_proxy_async_smem();  // the slots' last generic reads come before these copies
@@ -536,12 +516,6 @@ __device__ __forceinline__ float block_reduce(float v, bool is_max, float* red) 
 // chunks t, t + THREADS, ... of the row (8 channels each).
 constexpr int kMaxStages = 8;
 constexpr int kStageBudget = 48 * 1024;  // shared-memory bytes of one CTA's ring
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 
 // Modulation vectors of one chunk (zero without a table row).
 __device__ __forceinline__ void mod_chunk(const float* m, const ModNormArgs& a, int K, int c, float (&sh)[8],

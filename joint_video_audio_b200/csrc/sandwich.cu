@@ -33,11 +33,6 @@ namespace {
 constexpr int kMaxStages = 8;
 constexpr int kSortRows = 256;  // rows grouped by key at a time
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -46,9 +41,7 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// Sums (IS_MAX: maxima of non-negative values) of R rows over the CTA; one
-// barrier. `red` has a slot per warp, of 32, those past the last warp zero, and
-// is written again after another barrier at least.
+// Sum (IS_MAX: maximum of non-negative values) over the warp.
 template <bool IS_MAX>
 __device__ __forceinline__ float warp_reduce(float v) {
   if (IS_MAX) return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
@@ -56,7 +49,9 @@ __device__ __forceinline__ float warp_reduce(float v) {
   for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
 }
-// The sums of two rows share the exchanges: after the first one a lane carries
+// The same of R rows over the CTA; one barrier. `red` has a slot per warp, of 32,
+// those past the last warp zero, and is written again after another barrier at
+// least. The sums of two rows share the exchanges: after the first one a lane carries
 // row lane % 2, of itself and its neighbour (bf16 h, 32768 x 5376: 242 -> 229 us).
 template <bool IS_MAX, int R>
 __device__ __forceinline__ void cta_reduce(float (&v)[R], float (*red)[32]) {
