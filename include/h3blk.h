@@ -347,6 +347,9 @@ H3BLK_API int h3blk_gemm_fp4(const h3blk_fp4* A, const h3blk_fp4* B, int epilogu
  *   h_fp4        h as the operand of h3blk_gemm_fp4, quantised from its fp32
  *                values as by h3blk_quantize_fp4 (rotate as there). Exactly one
  *                of the two with norm_table, none without.
+ * With more than 2048 channels a rotated h takes longer than a bf16 h with
+ * h3blk_quantize_fp4 behind it (which rounds it to bf16 in between), an NV one
+ * about as long.
  * x_out, h and the parts of h_fp4 overlap nothing else, one another neither
  * (INVALID_ARG), but for x_out = x. */
 typedef struct {

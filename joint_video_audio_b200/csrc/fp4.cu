@@ -30,7 +30,7 @@ __device__ __forceinline__ float warp_max(float v) {  // of values that are not 
 //
 // Measured (32768 x 14336, 2.53 / 2.56 bytes a value): MX 205 us (5.8 TB/s, 89 %
 // of the copy rate), MX rotated 209 us, NV 219 us, NV rotated 285 us, the last
-// two bound by issue (2.6-2.7 instructions a cycle). One row per CTA at a time
+// two by their instructions and the latencies between them (2.6 a cycle of 4). One row per CTA at a time
 // without the ring took 240, 338, 379 and 467 us. Grouped (131072 x 256): MX 22
 // us, NV 27 us, one row at a time 47 and 64; groups of two rows of 5376: MX 86 us
 // as without, NV 127 instead of 98.

@@ -1,6 +1,11 @@
 """The 4-bit linear path and the sandwich norm for torch tensors (no arithmetic
 here): include/h3blk.h states the formats and the formulas, csrc/fp4_torch.cpp
-checks the tensors and makes the calls."""
+checks the tensors and makes the calls.
+
+Tensors are contiguous unless a call says otherwise. Outputs come from the caching
+allocator without torch's dispatcher: dispatch modes do not see them, deterministic
+mode does not fill them, and they carry no gradient. A kernel that gives up a wait
+is reported by check_fp4 alone."""
 from __future__ import annotations
 
 from functools import lru_cache
@@ -144,6 +149,9 @@ def sandwich_norm(x, y, tag, tidx, table, branch: int = 0, next_table=None, post
     `next_table`, the next layer's). h: "bf16", "mx" / "nv" (an Fp4Tensor, as
     quantize_fp4 of h's fp32 values; rotate as there) or None; without a next
     table there is no h after branch 1. x_out may be x. Returns (x_out, h).
+    With more than 2048 channels a rotated h takes longer than a "bf16" one with
+    quantize_fp4 behind it (which rounds it to bf16 in between), an "nv" one about
+    as long.
     h3blk_sandwich_norm."""
     if rotate and h not in FORMATS:
         raise ValueError("rotate is for an h in 4 bits")
