@@ -10,8 +10,11 @@
 
 namespace {
 // What the kernels of these calls report, on each device: a bit per kind of wait
-// that ran out, until h3blk_fp4_check takes it.
-__device__ int g_fp4_error;
+// that ran out, until h3blk_fp4_check takes it; and what it took.
+__device__ int g_fp4_error, g_fp4_taken;
+
+// (an exchange, so that no report of a kernel still running is lost)
+__global__ void take_error_kernel() { g_fp4_taken = atomicExch(&g_fp4_error, 0); }
 
 using h3api::aligned16;
 using h3api::cuda_status;
@@ -274,11 +277,12 @@ int h3blk_fp4_check(void* stream, int* status) {
   if (st != H3BLK_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int bits = 0;
-  if (cudaMemcpyAsync(&bits, d.err, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+  static std::mutex one;  // check at a time: they share the word that is taken to
+  std::lock_guard<std::mutex> lock(one);
+  take_error_kernel<<<1, 1, 0, s>>>();
+  if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&bits, g_fp4_taken, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess)
-    return H3BLK_ERR_CUDA;
-  // (cleared only where something stood: a report that comes in between is not lost)
-  if (bits && (cudaMemsetAsync(d.err, 0, sizeof(int), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess))
     return H3BLK_ERR_CUDA;
   *status = bits ? H3BLK_ERR_TIMEOUT : H3BLK_OK;
   return H3BLK_OK;
