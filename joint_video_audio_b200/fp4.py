@@ -2,7 +2,8 @@
 here): include/h3blk.h states the formats and the formulas, csrc/fp4_torch.cpp
 checks the tensors and makes the calls.
 
-Tensors are contiguous unless a call says otherwise. Outputs come from the caching
+Tensors are contiguous; quantize_fp4's x and a given `out` may have a row stride that
+is a multiple of 8. Outputs come from the caching
 allocator without torch's dispatcher: dispatch modes do not see them, deterministic
 mode does not fill them, and they carry no gradient. A kernel that gives up a wait
 is reported by check_fp4 alone."""

@@ -73,3 +73,30 @@ def test_sandwich_norm_of_several_widths(j, h):
 
 def test_rotate_quantize_of_several_widths(j):
     _in_threads([lambda x=_rows(4, k): j.rotate_quantize(x) for k in (7168, 14336, 5376, 16384)])
+
+
+def test_products_of_every_kernel_at_once(j):
+    """One row with split sums, 40 rows of SwiGLU, 128 unsplit and the pair kernel's
+    many, each behind its own quantisation, which their set-up overlaps, and one
+    thread of sandwich norms into a product."""
+    g = torch.Generator().manual_seed(3)
+
+    def product(m, n, k, swiglu):
+        x = torch.randn(m, k, generator=g).to(torch.bfloat16).cuda()
+        w = j.quantize_fp4((torch.randn(n, k, generator=g) / k ** 0.5).to(torch.bfloat16).cuda())
+        return lambda: (j.gemm_fp4(j.quantize_fp4(x), w, swiglu=swiglu),)
+
+    def chain():
+        x = torch.randn(300, 1024, generator=g).to(torch.bfloat16).cuda()
+        i, t = torch.zeros(300, dtype=torch.int32, device="cuda"), (0.3 * torch.randn(1, 1, 6, 1024, generator=g)).cuda()
+        w = j.quantize_fp4((torch.randn(512, 1024, generator=g) / 32).to(torch.bfloat16).cuda(), "mx")
+
+        def call():
+            x1, h = j.sandwich_norm(x, x, i, i, t, h="mx")
+            return x1, j.gemm_fp4(h, w)
+
+        return call
+
+    _in_threads([product(1, 1024, 5376, False), product(40, 2048, 2048, True), product(128, 21504, 512, False),
+                 product(2000, 1536, 768, True), chain()])
+    assert j.check_fp4() == j.H3BLK_OK
